@@ -444,6 +444,114 @@ rs_status rs_muon_orthogonalize(const rs_muon* muon, int32_t root, uint16_t* d_r
 rs_status rs_muon_apply(const rs_muon* muon, int32_t root, float* d_master, const uint16_t* d_root,
                         const rs_muon_hparams* hp, void* stream);
 
+/* -------------------------------------------------- training objectives
+ * The end of the forward pass and the start of the backward pass: losses
+ * over a model's logits, each with the gradient that the backward pass
+ * carries to the grad DBuffer.  (The pages start at the gradients; the
+ * objectives are this library's own, for post-training and for the MoE
+ * buckets, whose routers and output heads are among the planned tensors.)
+ *
+ * Logits are `rows` rows of `vocab` (or `experts`) values, row t at element
+ * offset t * ld, dtype RS_F32 or RS_BF16; the columns behind a row's values
+ * are neither read nor written.  d_dlogits has the same dtype and its own
+ * row stride ldd; it may be d_logits itself with ldd = ld (in place), and is
+ * otherwise disjoint from it; NULL asks for the loss alone.  Logits, their
+ * gradients and all other arrays need the alignment of their elements only.
+ * Row maxima and exponentials are binary32, sums over a row binary32 within
+ * a thread and binary64 across threads, and everything per row (logarithm,
+ * ratios, losses, their sums) binary64, rounded once to the output type, so
+ * results do not depend on timing: equal calls give equal bits.
+ *
+ * A row's token is d_target[t]; a value outside [0, vocab) (-1 by custom)
+ * marks a row without a token.  Such a row, a row of weight 0 and a row
+ * whose logits are all -inf take no part: nothing of theirs that is not
+ * finite reaches a result, their logp is 0 and their gradient row is 0.
+ * A token whose own logit is -inf in a row with others has logp -inf, and
+ * losses of it follow IEEE arithmetic; NaN or +inf logits give NaN.
+ *
+ * d_work: device scratch of at least the bytes the matching _bytes function
+ * gives, 16-byte aligned.  It carries nothing from call to call and needs no
+ * initialisation; calls that share one must be ordered by the caller.  The
+ * calls only launch kernels on `stream` (capturable in a HIP graph). */
+
+/* Scratch bytes of rs_token_logp and rs_policy_loss (n_seq = 0) and of
+ * rs_preference_loss (n_seq = 2 * n_pairs); 0 for sizes the calls refuse. */
+size_t rs_objective_bytes(int64_t rows, int64_t vocab, int64_t n_seq);
+
+/* d_logp[t] = log softmax(z_t / temperature)[d_target[t]], and with d_lse
+ * (nullable) d_lse[t] = log sum exp(z_t / temperature) (0 for a row that
+ * takes no part).  Errors: RS_EINVAL (NULL or misaligned pointer, negative
+ * rows, vocab outside 1..2^24, ld < vocab, temperature outside
+ * [2^-20, 2^20]),
+ * RS_EOVERFLOW (rows * ld beyond 2^50), RS_ENOMEM (bytes too small),
+ * RS_EHIP. */
+rs_status rs_token_logp(const void* d_logits, int32_t dtype, int64_t rows, int64_t vocab,
+                        int64_t ld, const int64_t* d_target, double temperature, float* d_logp,
+                        float* d_lse, void* d_work, size_t bytes, void* stream);
+
+typedef struct {
+    double temperature;         /* in [2^-20, 2^20] */
+    double clip_low, clip_high; /* the ratio is held in [1 - clip_low, 1 + clip_high] */
+    double kl_coef;             /* >= 0 */
+} rs_policy_hparams;
+
+/* Clipped policy loss with a KL term.  For every row with a token, with
+ * l = logp of the token at the temperature:
+ *   r  = exp(l - d_old_logp[t]),  A = d_advantage[t],
+ *   pg = max(-A r, -A min(max(r, 1 - clip_low), 1 + clip_high)),
+ *   kl = exp(ref - l) - (ref - l) - 1,  ref = d_ref_logp[t],
+ *   loss = sum_t d_weight[t] (pg_t + kl_coef kl_t).
+ * d_weight carries the mask and the averaging (0 for tokens that do not
+ * count, one over their number for a mean over tokens, ...).  A row's
+ * gradient passes through pg only where the ratio is not the clipped one
+ * (-A r >= the other branch).
+ * d_dlogits[t][i] = dloss/dz (as dtype); d_logp (nullable): l per row;
+ * d_stats: 4 floats, the loss, sum w pg, sum w kl and sum w over clipped
+ * rows.  d_ref_logp may be NULL when kl_coef is 0 (sum w kl is then 0).
+ * Errors: as rs_token_logp, and RS_EINVAL for hyper-parameters out of range
+ * or a d_dlogits that overlaps d_logits without being it. */
+rs_status rs_policy_loss(const void* d_logits, int32_t dtype, int64_t rows, int64_t vocab,
+                         int64_t ld, const int64_t* d_target, const float* d_old_logp,
+                         const float* d_ref_logp, const float* d_advantage,
+                         const float* d_weight, const rs_policy_hparams* hp, void* d_dlogits,
+                         int64_t ldd, float* d_logp, float* d_stats, void* d_work, size_t bytes,
+                         void* stream);
+
+enum { RS_PREF_SIGMOID = 0, RS_PREF_HINGE = 1, RS_PREF_IPO = 2 };
+
+typedef struct {
+    double temperature;     /* in [2^-20, 2^20] */
+    double beta;            /* > 0 */
+    double label_smoothing; /* in [0, 0.5); RS_PREF_SIGMOID only, else 0 */
+    double margin;          /* RS_PREF_SIGMOID and RS_PREF_HINGE, else 0 */
+    int32_t kind;           /* RS_PREF_* */
+    int32_t average;        /* 0: a sequence's sum of logp, 1: its mean */
+} rs_preference_hparams;
+
+/* Preference loss over n_pairs pairs of packed sequences.  Sequence s holds
+ * rows [d_start[s], d_start[s + 1]) (2 n_pairs + 1 ascending row numbers);
+ * sequence p < n_pairs is pair p's preferred one and n_pairs + p its other.
+ *   L_s = sum (or mean) of logp over the rows of s with a token (0 if none),
+ *   D_p = (L_p - ref_p) - (L_{n_pairs + p} - ref_{n_pairs + p}),
+ *         ref = d_ref_logp (2 n_pairs floats; NULL: 0),
+ *   h_p = beta D_p - margin,
+ *   RS_PREF_SIGMOID: -(1 - e) log s(h) - e log s(-h), e = label_smoothing,
+ *                    s the logistic function,
+ *   RS_PREF_HINGE:   max(0, 1 - h) (gradient 0 at h = 1),
+ *   RS_PREF_IPO:     (D - 1 / (2 beta))^2;
+ *   loss = sum_p d_weight[p] loss_p  (d_weight NULL: 1 / n_pairs each).
+ * A pair of weight 0 takes no part (its rows with logp 0, gradient 0).
+ * d_seq_logp (nullable): L_s, 2 n_pairs floats; d_stats: 3 floats, the
+ * loss, sum w h and sum w over pairs with h > 0.  Rows outside every
+ * sequence (before d_start[0], behind d_start[2 n_pairs]) are left as they
+ * were.  Errors: as rs_policy_loss; RS_EINVAL for n_pairs < 1. */
+rs_status rs_preference_loss(const void* d_logits, int32_t dtype, int64_t rows, int64_t vocab,
+                             int64_t ld, const int64_t* d_target, const int64_t* d_start,
+                             int64_t n_pairs, const float* d_ref_logp, const float* d_weight,
+                             const rs_preference_hparams* hp, void* d_dlogits, int64_t ldd,
+                             float* d_seq_logp, float* d_stats, void* d_work, size_t bytes,
+                             void* stream);
+
 /* Synchronises the stream and reports a device-side failure of the
  * one-launch split modes: RS_EHIP if a bounded wait for the other chunks of
  * a block gave up since the last check, or if the caller set the status

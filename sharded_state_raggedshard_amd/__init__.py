@@ -27,6 +27,7 @@ RS_ORDER_BY_SIZE = 2
 RS_ORDER_MASK = 0xff
 RS_ALIGN_CUT_UNIT = 0x100
 RS_SPLIT_TWO_PASS, RS_SPLIT_COOPERATIVE, RS_SPLIT_ORDERED = 0, 1, 2
+RS_PREF_SIGMOID, RS_PREF_HINGE, RS_PREF_IPO = 0, 1, 2
 RS_ALL = -1
 
 # every entry point declared in include/raggedshard.h
@@ -40,6 +41,7 @@ EXPORTS = (
     "rs_plan_check_device", "rs_plan_status_offset", "rs_last_error", "rs_version",
     "rs_muon_plan", "rs_muon_free", "rs_muon_layout", "rs_muon_device_bytes", "rs_muon_upload",
     "rs_muon_gather", "rs_muon_orthogonalize", "rs_muon_apply",
+    "rs_objective_bytes", "rs_token_logp", "rs_policy_loss", "rs_preference_loss",
 )
 
 
@@ -61,6 +63,17 @@ class rs_adam_hparams(C.Structure):
 
 class rs_muon_hparams(C.Structure):
     _fields_ = [("lr", C.c_double), ("momentum", C.c_double), ("weight_decay", C.c_double)]
+
+
+class rs_policy_hparams(C.Structure):
+    _fields_ = [("temperature", C.c_double), ("clip_low", C.c_double), ("clip_high", C.c_double),
+                ("kl_coef", C.c_double)]
+
+
+class rs_preference_hparams(C.Structure):
+    _fields_ = [("temperature", C.c_double), ("beta", C.c_double),
+                ("label_smoothing", C.c_double), ("margin", C.c_double), ("kind", C.c_int32),
+                ("average", C.c_int32)]
 
 
 _lib = None
@@ -115,6 +128,15 @@ def lib() -> C.CDLL:
         "rs_muon_gather": ([vp, i32, vp, vp, C.POINTER(rs_muon_hparams), vp, vp], C.c_int),
         "rs_muon_orthogonalize": ([vp, i32, vp, vp], C.c_int),
         "rs_muon_apply": ([vp, i32, vp, vp, C.POINTER(rs_muon_hparams), vp], C.c_int),
+        "rs_objective_bytes": ([i64, i64, i64], C.c_size_t),
+        "rs_token_logp": ([vp, i32, i64, i64, i64, vp, C.c_double, vp, vp, vp, C.c_size_t, vp],
+                          C.c_int),
+        "rs_policy_loss": ([vp, i32, i64, i64, i64, vp, vp, vp, vp, vp,
+                            C.POINTER(rs_policy_hparams), vp, i64, vp, vp, vp, C.c_size_t, vp],
+                           C.c_int),
+        "rs_preference_loss": ([vp, i32, i64, i64, i64, vp, vp, i64, vp, vp,
+                                C.POINTER(rs_preference_hparams), vp, i64, vp, vp, vp,
+                                C.c_size_t, vp], C.c_int),
         "rs_last_error": ([], C.c_char_p),
         "rs_version": ([], C.c_char_p),
     }
@@ -376,6 +398,51 @@ def rs_muon_apply(muon: int, root: int, master, root_buf, lr: float = 1e-3,
     hp = _muon_hp(lr, 0.0, weight_decay)
     _check(lib().rs_muon_apply(muon, root, _ptr(master), _ptr(root_buf), C.byref(hp),
                                _stream(stream)))
+
+
+def rs_objective_bytes(rows: int, vocab: int, n_seq: int = 0) -> int:
+    n = lib().rs_objective_bytes(rows, vocab, n_seq)
+    if n == 0:
+        raise RaggedShardError(RS_EINVAL, lib().rs_last_error().decode())
+    return int(n)
+
+
+def rs_token_logp(logits, dtype: int, rows: int, vocab: int, ld: int, target, logp, work,
+                  nbytes: int, lse=None, temperature: float = 1.0, stream=None) -> None:
+    """logits: rows x vocab of `dtype`, row stride ld elements; target: int64
+    token per row (outside [0, vocab): none); logp (and lse): fp32 per row."""
+    _check(lib().rs_token_logp(_ptr(logits), dtype, rows, vocab, ld, _ptr(target), temperature,
+                               _ptr(logp), _ptr(lse), _ptr(work), nbytes, _stream(stream)))
+
+
+def rs_policy_loss(logits, dtype: int, rows: int, vocab: int, ld: int, target, old_logp, ref_logp,
+                   advantage, weight, dlogits, ldd: int, logp, stats, work, nbytes: int,
+                   temperature: float = 1.0, clip_low: float = 0.2, clip_high: float = 0.2,
+                   kl_coef: float = 0.0, stream=None) -> None:
+    """fp32 per row: old_logp, ref_logp (None without a KL term), advantage,
+    weight, logp (or None).  dlogits (or None): as logits, row stride ldd.
+    stats: 4 fp32 (loss, policy part, KL part, clipped weight)."""
+    hp = rs_policy_hparams(temperature, clip_low, clip_high, kl_coef)
+    _check(lib().rs_policy_loss(_ptr(logits), dtype, rows, vocab, ld, _ptr(target),
+                                _ptr(old_logp), _ptr(ref_logp), _ptr(advantage), _ptr(weight),
+                                C.byref(hp), _ptr(dlogits), ldd, _ptr(logp), _ptr(stats),
+                                _ptr(work), nbytes, _stream(stream)))
+
+
+def rs_preference_loss(logits, dtype: int, rows: int, vocab: int, ld: int, target, start,
+                       n_pairs: int, ref_logp, weight, dlogits, ldd: int, seq_logp, stats, work,
+                       nbytes: int, temperature: float = 1.0, beta: float = 0.1,
+                       label_smoothing: float = 0.0, margin: float = 0.0,
+                       kind: int = RS_PREF_SIGMOID, average: bool = False, stream=None) -> None:
+    """start: int64 [2 n_pairs + 1] rows of the packed sequences (preferred
+    ones first); ref_logp (or None), seq_logp (or None): fp32 per sequence;
+    weight (or None): fp32 per pair; stats: 3 fp32 (loss, weighted h,
+    weight of the pairs with h > 0)."""
+    hp = rs_preference_hparams(temperature, beta, label_smoothing, margin, kind, int(average))
+    _check(lib().rs_preference_loss(_ptr(logits), dtype, rows, vocab, ld, _ptr(target),
+                                    _ptr(start), n_pairs, _ptr(ref_logp), _ptr(weight),
+                                    C.byref(hp), _ptr(dlogits), ldd, _ptr(seq_logp), _ptr(stats),
+                                    _ptr(work), nbytes, _stream(stream)))
 
 
 def rs_last_error() -> str:

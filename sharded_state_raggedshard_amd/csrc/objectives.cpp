@@ -1,0 +1,233 @@
+// C-ABI entry points of the training objectives: argument checks, scratch
+// layout and launches.  Every check happens before the first launch.
+#include <hip/hip_runtime_api.h>
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "objectives.hpp"
+#include "plan.hpp"
+#include "raggedshard.h"
+
+namespace {
+
+rs_status fail(rs_status st, std::string msg) { return rs::set_error(st, std::move(msg)); }
+
+rs_status hip_fail(hipError_t e, const char* what) {
+    return fail(RS_EHIP, std::string(what) + ": " + hipGetErrorString(e));
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
+
+constexpr int64_t kMaxElems = int64_t(1) << 50;
+constexpr int64_t kMaxPairs = int64_t(1) << 23;  // one workgroup each in one launch
+
+// Scratch: row statistics, token logits; for the preference loss also marks,
+// coefficients and the pairs' sums.
+struct Scratch {
+    size_t stat = 0, token = 0, mark = 0, coef = 0, terms = 0, bytes = 0;
+};
+
+Scratch scratch_of(int64_t rows, int64_t vocab, int64_t n_seq) {
+    Scratch s;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t p = at;
+        at = align256(at + n);
+        return p;
+    };
+    s.stat = take(size_t(rows) * rs::stat_parts(rows, vocab) * sizeof(float2));
+    s.token = take(size_t(rows) * sizeof(float));
+    if (n_seq > 0) {
+        s.mark = take(size_t(rows) * sizeof(int32_t));
+        s.coef = take(size_t(rows) * sizeof(float));
+        s.terms = take(size_t(n_seq / 2) * 3 * sizeof(double));
+    }
+    s.bytes = std::max<size_t>(at, 256);
+    return s;
+}
+
+// Checks what every objective takes; fills `a` and its scratch pointers.
+rs_status check_logits(const void* z, int32_t dtype, int64_t rows, int64_t width, int64_t ld,
+                       const void* work) {
+    if (dtype != RS_F32 && dtype != RS_BF16) return fail(RS_EINVAL, "unknown dtype");
+    if (rows < 0) return fail(RS_EINVAL, "negative number of rows");
+    if (ld < width) return fail(RS_EINVAL, "row stride below the row's length");
+    if (rows > kMaxElems / ld) return fail(RS_EOVERFLOW, "rows * ld beyond 2^50 elements");
+    if (rows > 0 && !z) return fail(RS_EINVAL, "NULL argument");
+    if (!aligned(z, dtype == RS_F32 ? 4 : 2)) return fail(RS_EINVAL, "misaligned pointer");
+    if (!work) return fail(RS_EINVAL, "NULL argument");
+    if (!aligned(work, 16)) return fail(RS_EINVAL, "workspace not 16-byte aligned");
+    return RS_OK;
+}
+
+// d must be z with the same stride, or share no element with it.
+rs_status check_gradient(const void* z, const void* d, int32_t dtype, int64_t rows, int64_t width,
+                         int64_t ld, int64_t ldd) {
+    if (!d) return RS_OK;
+    const int64_t size = dtype == RS_F32 ? 4 : 2;
+    if (!aligned(d, size_t(size))) return fail(RS_EINVAL, "misaligned pointer");
+    if (ldd < width) return fail(RS_EINVAL, "row stride below the row's length");
+    if (rows > kMaxElems / ldd) return fail(RS_EOVERFLOW, "rows * ldd beyond 2^50 elements");
+    if (rows == 0) return RS_OK;
+    const uintptr_t z0 = reinterpret_cast<uintptr_t>(z), d0 = reinterpret_cast<uintptr_t>(d);
+    const uintptr_t z1 = z0 + uintptr_t(((rows - 1) * ld + width) * size);
+    const uintptr_t d1 = d0 + uintptr_t(((rows - 1) * ldd + width) * size);
+    if (d1 <= z0 || z1 <= d0) return RS_OK;
+    if (ld == ldd && d0 == z0) return RS_OK;
+    if (ld == ldd) {  // columns of one array, side by side
+        const uintptr_t step = uintptr_t(ld * size), row = uintptr_t(width * size);
+        const uintptr_t off = d0 >= z0 ? (d0 - z0) % step : (step - (z0 - d0) % step) % step;
+        if (off >= row && off + row <= step) return RS_OK;
+    }
+    return fail(RS_EINVAL, "the gradient overlaps the logits without being them");
+}
+
+rs_status check_temperature(double t) {
+    if (!(t >= 0x1p-20 && t <= 0x1p20)) return fail(RS_EINVAL, "temperature outside [2^-20, 2^20]");
+    return RS_OK;
+}
+
+rs_status fill_rows(const void* z, int32_t dtype, int64_t rows, int64_t vocab, int64_t ld,
+                    const int64_t* target, double temperature, void* work, size_t bytes,
+                    int64_t n_seq, rs::LogitRows& a, Scratch& sc) {
+    if (vocab < 1 || vocab > rs::kMaxVocab) return fail(RS_EINVAL, "vocab outside 1..2^24");
+    rs_status st = check_logits(z, dtype, rows, vocab, ld, work);
+    if (st != RS_OK) return st;
+    if (rows > 0 && !target) return fail(RS_EINVAL, "NULL argument");
+    if (!aligned(target, 8)) return fail(RS_EINVAL, "misaligned pointer");
+    st = check_temperature(temperature);
+    if (st != RS_OK) return st;
+    sc = scratch_of(rows, vocab, n_seq);
+    if (bytes < sc.bytes)
+        return fail(RS_ENOMEM, "workspace of " + std::to_string(bytes) + " bytes; the call needs " +
+                                   std::to_string(sc.bytes));
+    uint8_t* w = static_cast<uint8_t*>(work);
+    a.z = z;
+    a.f32 = dtype == RS_F32;
+    a.rows = rows;
+    a.vocab = vocab;
+    a.ld = ld;
+    a.target = target;
+    a.weight = nullptr;
+    a.scale = 1.0 / temperature;
+    a.parts = rs::stat_parts(rows, vocab);
+    a.stat = reinterpret_cast<float2*>(w + sc.stat);
+    a.token = reinterpret_cast<float*>(w + sc.token);
+    return RS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t rs_objective_bytes(int64_t rows, int64_t vocab, int64_t n_seq) {
+    if (rows < 0 || vocab < 1 || vocab > rs::kMaxVocab || rows > kMaxElems / vocab || n_seq < 0 ||
+        n_seq > 2 * kMaxPairs) {
+        fail(RS_EINVAL, "sizes out of range");
+        return 0;
+    }
+    return scratch_of(rows, vocab, n_seq).bytes;
+}
+
+rs_status rs_token_logp(const void* d_logits, int32_t dtype, int64_t rows, int64_t vocab,
+                        int64_t ld, const int64_t* d_target, double temperature, float* d_logp,
+                        float* d_lse, void* d_work, size_t bytes, void* stream) {
+    rs::LogitRows a;
+    Scratch sc;
+    rs_status st = fill_rows(d_logits, dtype, rows, vocab, ld, d_target, temperature, d_work, bytes,
+                             0, a, sc);
+    if (st != RS_OK) return st;
+    if (rows > 0 && !d_logp) return fail(RS_EINVAL, "NULL argument");
+    if (!aligned(d_logp, 4) || !aligned(d_lse, 4)) return fail(RS_EINVAL, "misaligned pointer");
+    hipError_t e = rs::launch_token_logp(a, d_logp, d_lse, as_stream(stream));
+    if (e != hipSuccess) return hip_fail(e, "token_logp launch");
+    return RS_OK;
+}
+
+rs_status rs_policy_loss(const void* d_logits, int32_t dtype, int64_t rows, int64_t vocab,
+                         int64_t ld, const int64_t* d_target, const float* d_old_logp,
+                         const float* d_ref_logp, const float* d_advantage,
+                         const float* d_weight, const rs_policy_hparams* hp, void* d_dlogits,
+                         int64_t ldd, float* d_logp, float* d_stats, void* d_work, size_t bytes,
+                         void* stream) {
+    if (!hp || !d_stats) return fail(RS_EINVAL, "NULL argument");
+    rs::LogitRows a;
+    Scratch sc;
+    rs_status st = fill_rows(d_logits, dtype, rows, vocab, ld, d_target, hp->temperature, d_work,
+                             bytes, 0, a, sc);
+    if (st != RS_OK) return st;
+    if (!(hp->clip_low >= 0.0 && hp->clip_low <= 1.0) ||
+        !(hp->clip_high >= 0.0 && std::isfinite(hp->clip_high)) ||
+        !(hp->kl_coef >= 0.0 && std::isfinite(hp->kl_coef)))
+        return fail(RS_EINVAL, "hyper-parameters out of range");
+    if (rows > 0 && (!d_old_logp || !d_advantage || !d_weight)) return fail(RS_EINVAL, "NULL argument");
+    if (rows > 0 && hp->kl_coef != 0.0 && !d_ref_logp)
+        return fail(RS_EINVAL, "a KL term needs d_ref_logp");
+    if (!aligned(d_old_logp, 4) || !aligned(d_ref_logp, 4) || !aligned(d_advantage, 4) ||
+        !aligned(d_weight, 4) || !aligned(d_logp, 4) || !aligned(d_stats, 4))
+        return fail(RS_EINVAL, "misaligned pointer");
+    st = check_gradient(d_logits, d_dlogits, dtype, rows, vocab, ld, ldd);
+    if (st != RS_OK) return st;
+    a.weight = d_weight;
+    rs::PolicyTerms t;
+    t.old_logp = d_old_logp;
+    t.ref_logp = d_ref_logp;
+    t.advantage = d_advantage;
+    t.lo = 1.0 - hp->clip_low;
+    t.hi = 1.0 + hp->clip_high;
+    t.kl_coef = hp->kl_coef;
+    hipError_t e = rs::launch_policy(a, t, d_dlogits, ldd, d_logp, d_stats, as_stream(stream));
+    if (e != hipSuccess) return hip_fail(e, "policy_loss launch");
+    return RS_OK;
+}
+
+rs_status rs_preference_loss(const void* d_logits, int32_t dtype, int64_t rows, int64_t vocab,
+                             int64_t ld, const int64_t* d_target, const int64_t* d_start,
+                             int64_t n_pairs, const float* d_ref_logp, const float* d_weight,
+                             const rs_preference_hparams* hp, void* d_dlogits, int64_t ldd,
+                             float* d_seq_logp, float* d_stats, void* d_work, size_t bytes,
+                             void* stream) {
+    if (!hp || !d_stats || !d_start) return fail(RS_EINVAL, "NULL argument");
+    if (n_pairs < 1 || n_pairs > kMaxPairs) return fail(RS_EINVAL, "number of pairs outside 1..2^23");
+    rs::LogitRows a;
+    Scratch sc;
+    rs_status st = fill_rows(d_logits, dtype, rows, vocab, ld, d_target, hp->temperature, d_work,
+                             bytes, 2 * n_pairs, a, sc);
+    if (st != RS_OK) return st;
+    if (hp->kind != RS_PREF_SIGMOID && hp->kind != RS_PREF_HINGE && hp->kind != RS_PREF_IPO)
+        return fail(RS_EINVAL, "unknown loss kind");
+    if (!(hp->beta > 0.0) || !std::isfinite(hp->beta) || !std::isfinite(hp->margin) ||
+        !(hp->label_smoothing >= 0.0 && hp->label_smoothing < 0.5) ||
+        (hp->average != 0 && hp->average != 1) ||
+        (hp->kind != RS_PREF_SIGMOID && hp->label_smoothing != 0.0) ||
+        (hp->kind == RS_PREF_IPO && hp->margin != 0.0))
+        return fail(RS_EINVAL, "hyper-parameters out of range");
+    if (!aligned(d_start, 8) || !aligned(d_ref_logp, 4) || !aligned(d_weight, 4) ||
+        !aligned(d_seq_logp, 4) || !aligned(d_stats, 4))
+        return fail(RS_EINVAL, "misaligned pointer");
+    st = check_gradient(d_logits, d_dlogits, dtype, rows, vocab, ld, ldd);
+    if (st != RS_OK) return st;
+    uint8_t* w = static_cast<uint8_t*>(d_work);
+    rs::PreferenceTerms t;
+    t.start = d_start;
+    t.pairs = n_pairs;
+    t.ref_logp = d_ref_logp;
+    t.weight = d_weight;
+    t.beta = hp->beta;
+    t.smoothing = hp->label_smoothing;
+    t.margin = hp->margin;
+    t.kind = hp->kind;
+    t.average = hp->average;
+    t.mark = reinterpret_cast<int32_t*>(w + sc.mark);
+    t.coef = reinterpret_cast<float*>(w + sc.coef);
+    t.terms = reinterpret_cast<double*>(w + sc.terms);
+    hipError_t e = rs::launch_preference(a, t, d_dlogits, ldd, d_seq_logp, d_stats, as_stream(stream));
+    if (e != hipSuccess) return hip_fail(e, "preference_loss launch");
+    return RS_OK;
+}
+
+}  // extern "C"

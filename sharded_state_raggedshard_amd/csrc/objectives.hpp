@@ -1,0 +1,56 @@
+// Training objectives: the launch arguments that objectives.cpp fills after
+// its checks, and the launchers of objective_kernels.hip.
+#pragma once
+#include <hip/hip_runtime_api.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace rs {
+
+constexpr int64_t kMaxVocab = int64_t(1) << 24;
+
+// Rows of logits and, per row, what the kernels keep of them in scratch.
+struct LogitRows {
+    const void* z;
+    int32_t f32;  // 1: binary32, 0: bf16
+    int64_t rows, vocab, ld;
+    const int64_t* target;
+    const float* weight;  // per row (policy) or nullptr
+    double scale;         // 1 / temperature
+    // scratch: `parts` (max, sum) pairs and the token's logit per row
+    int32_t parts;
+    float2* stat;
+    float* token;
+};
+
+struct PolicyTerms {
+    const float* old_logp;
+    const float* ref_logp;  // nullable: no KL term
+    const float* advantage;
+    double lo, hi, kl_coef;  // the ratio's bounds
+};
+
+struct PreferenceTerms {
+    const int64_t* start;
+    int64_t pairs;
+    const float* ref_logp;  // nullable
+    const float* weight;    // nullable
+    double beta, smoothing, margin;
+    int32_t kind, average;
+    // scratch: a mark and a coefficient per row, three sums per pair
+    int32_t* mark;
+    float* coef;
+    double* terms;
+};
+
+// Parts a row is split into for its statistics.
+int32_t stat_parts(int64_t rows, int64_t vocab);
+
+hipError_t launch_token_logp(const LogitRows& a, float* logp, float* lse, hipStream_t s);
+hipError_t launch_policy(const LogitRows& a, const PolicyTerms& t, void* d, int64_t ldd,
+                         float* logp, float* stats, hipStream_t s);
+hipError_t launch_preference(const LogitRows& a, const PreferenceTerms& t, void* d, int64_t ldd,
+                             float* seq_logp, float* stats, hipStream_t s);
+
+}  // namespace rs
