@@ -552,6 +552,45 @@ rs_status rs_preference_loss(const void* d_logits, int32_t dtype, int64_t rows, 
                              float* d_seq_logp, float* d_stats, void* d_work, size_t bytes,
                              void* stream);
 
+enum { RS_SCORE_SOFTMAX = 0, RS_SCORE_SIGMOID = 1 };
+
+typedef struct {
+    double balance_coef; /* >= 0 */
+    double z_coef;       /* >= 0; 0 with RS_SCORE_SIGMOID */
+    int32_t score;       /* RS_SCORE_* */
+    int32_t reserved;    /* must be 0 */
+} rs_balance_hparams;
+
+/* Scratch bytes of rs_router_balance; 0 for sizes it refuses. */
+size_t rs_router_balance_bytes(int64_t rows, int32_t experts, int64_t n_seq);
+
+/* Counts, mean probabilities and load-balance loss of a router whose logits
+ * are d_logits (rows x experts) and whose choices are d_topk (k expert ids a
+ * row, row stride ldk; an id outside [0, experts) counts nowhere, one given
+ * twice counts twice).  Sequence s holds rows [d_start[s], d_start[s + 1])
+ * (n_seq + 1 ascending row numbers; NULL with n_seq = 1: all rows); rows
+ * with d_mask[t] = 0 (bytes; NULL: none) take no part, their gradient is 0.
+ * Over the n tokens that do, per sequence:
+ *   p = softmax(z)  (RS_SCORE_SOFTMAX)  or  s(z_e) / sum s(z)
+ *       (RS_SCORE_SIGMOID, s the logistic function),
+ *   c_e = count of e,  f_e = experts c_e / (k n),  P_e = sum_t p_te / n,
+ *   loss = balance_coef sum_e f_e P_e + z_coef sum_t lse_t^2 / n,
+ * summed over the sequences (fold a mean over them into the coefficients).
+ * The counts pass no gradient; d_dlogits (nullable) is dloss/dz as dtype.
+ * A row whose logits are all -inf has p = 0 and gradient 0 but counts
+ * in n.  d_counts, d_mean_prob: n_seq x experts (int32, fp32; 0 for a sequence
+ * without tokens); d_stats: 2 floats, the balance and the z part of the
+ * loss.  Rows outside every sequence are left as they were.
+ * Errors: RS_EINVAL (as rs_policy_loss; experts outside 1..1024, k outside
+ * 1..experts, n_seq outside 1..2^16), RS_EOVERFLOW (rows * k beyond
+ * 2^31 - 1), RS_ENOMEM, RS_EHIP. */
+rs_status rs_router_balance(const void* d_logits, int32_t dtype, int64_t rows, int32_t experts,
+                            int64_t ld, const int64_t* d_topk, int32_t k, int64_t ldk,
+                            const uint8_t* d_mask, const int64_t* d_start, int64_t n_seq,
+                            const rs_balance_hparams* hp, void* d_dlogits, int64_t ldd,
+                            int32_t* d_counts, float* d_mean_prob, float* d_stats, void* d_work,
+                            size_t bytes, void* stream);
+
 /* Synchronises the stream and reports a device-side failure of the
  * one-launch split modes: RS_EHIP if a bounded wait for the other chunks of
  * a block gave up since the last check, or if the caller set the status

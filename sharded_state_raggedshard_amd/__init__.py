@@ -28,6 +28,7 @@ RS_ORDER_MASK = 0xff
 RS_ALIGN_CUT_UNIT = 0x100
 RS_SPLIT_TWO_PASS, RS_SPLIT_COOPERATIVE, RS_SPLIT_ORDERED = 0, 1, 2
 RS_PREF_SIGMOID, RS_PREF_HINGE, RS_PREF_IPO = 0, 1, 2
+RS_SCORE_SOFTMAX, RS_SCORE_SIGMOID = 0, 1
 RS_ALL = -1
 
 # every entry point declared in include/raggedshard.h
@@ -42,6 +43,7 @@ EXPORTS = (
     "rs_muon_plan", "rs_muon_free", "rs_muon_layout", "rs_muon_device_bytes", "rs_muon_upload",
     "rs_muon_gather", "rs_muon_orthogonalize", "rs_muon_apply",
     "rs_objective_bytes", "rs_token_logp", "rs_policy_loss", "rs_preference_loss",
+    "rs_router_balance_bytes", "rs_router_balance",
 )
 
 
@@ -74,6 +76,11 @@ class rs_preference_hparams(C.Structure):
     _fields_ = [("temperature", C.c_double), ("beta", C.c_double),
                 ("label_smoothing", C.c_double), ("margin", C.c_double), ("kind", C.c_int32),
                 ("average", C.c_int32)]
+
+
+class rs_balance_hparams(C.Structure):
+    _fields_ = [("balance_coef", C.c_double), ("z_coef", C.c_double), ("score", C.c_int32),
+                ("reserved", C.c_int32)]
 
 
 _lib = None
@@ -137,6 +144,10 @@ def lib() -> C.CDLL:
         "rs_preference_loss": ([vp, i32, i64, i64, i64, vp, vp, i64, vp, vp,
                                 C.POINTER(rs_preference_hparams), vp, i64, vp, vp, vp,
                                 C.c_size_t, vp], C.c_int),
+        "rs_router_balance_bytes": ([i64, i32, i64], C.c_size_t),
+        "rs_router_balance": ([vp, i32, i64, i32, i64, vp, i32, i64, vp, vp, i64,
+                               C.POINTER(rs_balance_hparams), vp, i64, vp, vp, vp, vp,
+                               C.c_size_t, vp], C.c_int),
         "rs_last_error": ([], C.c_char_p),
         "rs_version": ([], C.c_char_p),
     }
@@ -443,6 +454,28 @@ def rs_preference_loss(logits, dtype: int, rows: int, vocab: int, ld: int, targe
                                     _ptr(start), n_pairs, _ptr(ref_logp), _ptr(weight),
                                     C.byref(hp), _ptr(dlogits), ldd, _ptr(seq_logp), _ptr(stats),
                                     _ptr(work), nbytes, _stream(stream)))
+
+
+def rs_router_balance_bytes(rows: int, experts: int, n_seq: int = 1) -> int:
+    n = lib().rs_router_balance_bytes(rows, experts, n_seq)
+    if n == 0:
+        raise RaggedShardError(RS_EINVAL, lib().rs_last_error().decode())
+    return int(n)
+
+
+def rs_router_balance(logits, dtype: int, rows: int, experts: int, ld: int, topk, k: int, ldk: int,
+                      mask, start, n_seq: int, dlogits, ldd: int, counts, mean_prob, stats, work,
+                      nbytes: int, balance_coef: float = 1e-2, z_coef: float = 0.0,
+                      score: int = RS_SCORE_SOFTMAX, stream=None) -> None:
+    """topk: int64 [rows, k] expert ids (row stride ldk); mask (or None): one
+    byte per row; start (or None: one sequence): int64 [n_seq + 1]; dlogits
+    (or None): as logits, row stride ldd; counts: int32, mean_prob: fp32
+    [n_seq, experts]; stats: 2 fp32 (balance part, z part)."""
+    hp = rs_balance_hparams(balance_coef, z_coef, score, 0)
+    _check(lib().rs_router_balance(_ptr(logits), dtype, rows, experts, ld, _ptr(topk), k, ldk,
+                                   _ptr(mask), _ptr(start), n_seq, C.byref(hp), _ptr(dlogits), ldd,
+                                   _ptr(counts), _ptr(mean_prob), _ptr(stats), _ptr(work), nbytes,
+                                   _stream(stream)))
 
 
 def rs_last_error() -> str:

@@ -124,3 +124,35 @@ def test_scratch_sizes():
     for bad in ((-1, 10, 0), (10, 0, 0), (10, (1 << 24) + 1, 0), (1 << 60, 8, 0), (10, 10, -2)):
         with pytest.raises(rs.RaggedShardError):
             rs.rs_objective_bytes(*bad)
+
+
+def _balance(**kw):
+    a = dict(logits=P, dtype=rs.RS_F32, rows=4, experts=100, ld=100, topk=P, k=2, ldk=2, mask=P,
+             start=P, n_seq=3, dlogits=P + (1 << 16), ldd=100, counts=P, mean_prob=P, stats=P, work=P,
+             nbytes=WORK, stream=0)
+    a.update(kw)
+    rs.rs_router_balance(**a)
+
+
+def test_router_balance_arguments_are_checked():
+    for name in ("logits", "topk", "counts", "mean_prob", "stats", "work", "start"):
+        _expect(rs.RS_EINVAL, _balance, **{name: None})
+    for name in ("logits", "topk", "counts", "mean_prob", "stats", "work", "start", "dlogits"):
+        _expect(rs.RS_EINVAL, _balance, **{name: P + (1 << 16) + 1})
+    for kw in (dict(dtype=2), dict(rows=-1), dict(experts=0, ld=100), dict(experts=1025, ld=2000, ldd=2000),
+               dict(ld=99), dict(ldd=99), dict(k=0), dict(k=101, ldk=101), dict(ldk=1), dict(n_seq=0),
+               dict(n_seq=(1 << 16) + 1), dict(balance_coef=float("nan")), dict(balance_coef=-1.0),
+               dict(z_coef=float("inf")), dict(z_coef=-1.0), dict(score=2),
+               dict(score=rs.RS_SCORE_SIGMOID, z_coef=0.1), dict(dlogits=P + 4), dict(dlogits=P, ldd=101)):
+        _expect(rs.RS_EINVAL, _balance, **kw)
+    _expect(rs.RS_EOVERFLOW, _balance, rows=1 << 30, k=4, ldk=4, dlogits=None)
+    _expect(rs.RS_EOVERFLOW, _balance, rows=1 << 44, dlogits=None)
+    _expect(rs.RS_EOVERFLOW, _balance, ldk=1 << 50, dlogits=None)
+    _expect(rs.RS_ENOMEM, _balance, nbytes=255)
+    hp = rs.rs_balance_hparams(0.1, 0.0, 0, 1)
+    assert rs.lib().rs_router_balance(P, 0, 4, 100, 100, P, 2, 2, P, P, 3, C.byref(hp), None, 100, P, P, P,
+                                      P, C.c_size_t(WORK), None) == rs.RS_EINVAL
+    assert rs.rs_router_balance_bytes(0, 1, 1) > 0
+    for bad in ((-1, 8, 1), (1, 0, 1), (1, 1025, 1), (1, 8, 0), (1, 8, 1 << 17)):
+        with pytest.raises(rs.RaggedShardError):
+            rs.rs_router_balance_bytes(*bad)
