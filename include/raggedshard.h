@@ -457,10 +457,10 @@ rs_status rs_muon_apply(const rs_muon* muon, int32_t root, float* d_master, cons
  * row stride ldd; it may be d_logits itself with ldd = ld (in place), and is
  * otherwise disjoint from it; NULL asks for the loss alone.  Logits, their
  * gradients and all other arrays need the alignment of their elements only.
- * Row maxima and exponentials are binary32, sums over a row binary32 within
- * a thread and binary64 across threads, and everything per row (logarithm,
- * ratios, losses, their sums) binary64, rounded once to the output type, so
- * results do not depend on timing: equal calls give equal bits.
+ * Exponentials are binary32, sums over a row binary64 (of up to 8 terms added
+ * in binary32), and everything per row (logarithm, ratios, losses, their
+ * sums) binary64, rounded once to the output type.  Sums are in a fixed
+ * order: equal calls give equal bits.
  *
  * A row's token is d_target[t]; a value outside [0, vocab) (-1 by custom)
  * marks a row without a token.  Such a row, a row of weight 0 and a row

@@ -2,10 +2,12 @@
 // log-probability, the clipped policy loss and the preference loss with
 // their logits' gradients.
 //
-// A row's softmax needs its maximum m and s = sum exp((z - m) / T).  With
-// k = log2(e) / T rounded to binary32 a term is exp2((z - m) k).  (Folding m
-// into one fused multiply-add, z k - m k, saves an instruction but overflows
-// on masks of the type's lowest value.)
+// A row's softmax needs its maximum m and s = sum exp((z - m) / T).  A term
+// is exp2((z - m) k), k = log2(e) / T in two binary32 pieces: one alone
+// would shift every term the same way (up to 2^-24 |z - m| / T, so the
+// row's logarithm with them), where the product's own rounding averages out.
+// (Folding m into one fused multiply-add, z k - m k, saves an instruction
+// but overflows on masks of the type's lowest value.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -24,83 +26,99 @@ using namespace rows;
 // that -inf values give exp2(-inf) = 0.
 __device__ __forceinline__ float reference(float m) { return m == kNegInf ? 0.0f : m; }
 
-__device__ __forceinline__ float term(float x, float r, float k) {
-    return exp2_fast((x - r) * k);
+__device__ __forceinline__ float term(float x, float r, ExpScale k) {
+    const float d = x - r;
+    return exp2_fast(__builtin_fmaf(d, k.hi, d * k.lo));
 }
 
-// Joins (m2, s2) into (m, s).
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float k) {
-    const float M = fmaxf(m, m2), r = reference(M);
-    s = s * term(m, r, k) + s2 * term(m2, r, k);
-    m = M;
-}
+// Running maximum and sum.  The sum is binary64: where one term is nearly
+// the whole row, as a trained model's are, a binary32 sum would round away
+// the rest that 1 - p is made of.  It takes N terms at a time, added up in
+// binary32.
+struct Running {
+    float m = kNegInf;
+    double s = 0.0;
 
-// Adds N values to (m, s).
-template <int N>
-__device__ __forceinline__ void take(float& m, float& s, const float (&x)[N], float k) {
-    float v = x[0];
+    template <int N>
+    __device__ __forceinline__ void take(const float (&x)[N], ExpScale k) {
+        float v = x[0];
 #pragma unroll
-    for (int i = 1; i < N; ++i) v = fmaxf(v, x[i]);
-    const float M = fmaxf(m, v), r = reference(M);
-    float a = s * term(m, r, k), b = 0.0f;
+        for (int i = 1; i < N; ++i) v = fmaxf(v, x[i]);
+        const float M = fmaxf(m, v), r = reference(M);
+        float a = 0.0f, b = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        a += term(x[i], r, k);
-        if (i + 1 < N) b += term(x[i + 1], r, k);
+        for (int i = 0; i < N; i += 2) {
+            a += term(x[i], r, k);
+            if (i + 1 < N) b += term(x[i + 1], r, k);
+        }
+        s = __builtin_fma(s, (double)term(m, r, k), (double)(a + b));
+        m = M;
     }
-    s = a + b;
-    m = M;
-}
 
-// (m, s) over the workgroup, in a fixed order; valid in every thread.
+    __device__ __forceinline__ void join(float m2, double s2, ExpScale k) {
+        const float M = fmaxf(m, m2), r = reference(M);
+        s = s * (double)term(m, r, k) + s2 * (double)term(m2, r, k);
+        m = M;
+    }
+};
+
+// The Running of a whole workgroup, in a fixed order; valid in every thread.
+// lds: 2 doubles per wave.
 template <int NT>
-__device__ __forceinline__ void wg_join(float& m, float& s, float k, float* lds) {
+__device__ __forceinline__ void wg_join(Running& x, ExpScale k, double* lds) {
+    float M = x.m;
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1)
-        join(m, s, __shfl_xor(m, off, 64), __shfl_xor(s, off, 64), k);
+    for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
+    x.s *= (double)term(x.m, reference(M), k);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) x.s += __shfl_xor(x.s, off, 64);
+    x.m = M;
     if (NT == 64) return;
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
-        lds[2 * wave] = m;
-        lds[2 * wave + 1] = s;
+        lds[2 * wave] = x.s;
+        lds[2 * wave + 1] = (double)x.m;
     }
     __syncthreads();
-    float M = kNegInf;
+    M = kNegInf;
 #pragma unroll
-    for (int w = 0; w < NT / 64; ++w) M = fmaxf(M, lds[2 * w]);
-    const float r = reference(M);
-    float S = 0.0f;
+    for (int w = 0; w < NT / 64; ++w) M = fmaxf(M, (float)lds[2 * w + 1]);
+    double S = 0.0;
 #pragma unroll
-    for (int w = 0; w < NT / 64; ++w) S += lds[2 * w + 1] * term(lds[2 * w], r, k);
+    for (int w = 0; w < NT / 64; ++w)
+        S += lds[2 * w] * (double)term((float)lds[2 * w + 1], reference(M), k);
     __syncthreads();
-    m = M;
-    s = S;
+    x.m = M;
+    x.s = S;
 }
 
 // What the statistics of a row come to.
 struct RowEnd {
-    float r;       // what the exponentials subtract
+    float m, r;    // maximum; what the exponentials subtract
     float inv;     // 1 / sum
+    double s;
     double lse_m;  // log sum exp((z - m) / T)
-    float m;
     bool empty;    // nothing but -inf
 };
 
-__device__ __forceinline__ RowEnd row_end(float m, float s) {
+__device__ __forceinline__ RowEnd row_end(const Running& x) {
     RowEnd e;
-    e.m = m;
-    e.empty = m == kNegInf && s == 0.0f;
-    e.r = reference(m);
-    e.inv = 1.0f / s;
-    e.lse_m = e.empty ? 0.0 : log((double)s);
+    e.m = x.m;
+    e.s = x.s;
+    e.empty = x.m == kNegInf && x.s == 0.0;
+    e.r = reference(x.m);
+    e.inv = (float)(1.0 / x.s);
+    e.lse_m = e.empty ? 0.0 : log(x.s);
     return e;
 }
 
-__device__ __forceinline__ RowEnd row_of(const LogitRows& a, int64_t row, float k) {
-    const float2* p = a.stat + row * a.parts;
-    float m = p[0].x, s = p[0].y;
-    for (int i = 1; i < a.parts; ++i) join(m, s, p[i].x, p[i].y, k);
-    return row_end(m, s);
+__device__ __forceinline__ RowEnd row_of(const LogitRows& a, int64_t row, ExpScale k) {
+    const RowStat* p = a.stat + row * a.parts;
+    Running x;
+    x.m = p[0].m;
+    x.s = p[0].s;
+    for (int i = 1; i < a.parts; ++i) x.join(p[i].m, p[i].s, k);
+    return row_end(x);
 }
 
 __device__ __forceinline__ double logp_of(const RowEnd& e, float token, double scale) {
@@ -110,10 +128,6 @@ __device__ __forceinline__ double logp_of(const RowEnd& e, float token, double s
 __device__ __forceinline__ bool has_token(const LogitRows& a, int64_t row) {
     const int64_t y = a.target[row];
     return y >= 0 && y < a.vocab && (!a.weight || a.weight[row] != 0.0f);
-}
-
-__device__ __forceinline__ float exponent_scale(double scale) {
-    return (float)(scale * 1.44269504088896340736);
 }
 
 // --------------------------------------------------------- row statistics
@@ -126,9 +140,9 @@ enum { MARK_OUTSIDE = 0, MARK_ZERO = 1, MARK_TOKEN = 2 };
 template <typename T, int NT, bool PREF>
 __global__ __launch_bounds__(NT) void row_stats_kernel(LogitRows a, PreferenceTerms t) {
     constexpr int N = Vec<T>::n, U = 4;
-    __shared__ float lds[2 * (NT / 64)];
+    __shared__ double lds[2 * (NT / 64)];
     const int tid = threadIdx.x;
-    const float k = exponent_scale(a.scale);
+    const ExpScale k = a.k;
     const int64_t items = a.rows * a.parts;
     const int64_t nv = a.vocab / N;
     const int64_t per = (nv + a.parts - 1) / a.parts;
@@ -147,7 +161,7 @@ __global__ __launch_bounds__(NT) void row_stats_kernel(LogitRows a, PreferenceTe
         }
         if (!live) continue;
         const T* z = static_cast<const T*>(a.z) + row * a.ld;
-        float m = kNegInf, s = 0.0f;
+        Running run;
         const int64_t v0 = part * per, v1 = min(nv, v0 + per);
         int64_t v = v0 + tid;
         for (; v + (U - 1) * NT < v1; v += U * NT) {
@@ -158,21 +172,21 @@ __global__ __launch_bounds__(NT) void row_stats_kernel(LogitRows a, PreferenceTe
             for (int u = 0; u < U; ++u) {
                 float x[N];
                 Vec<T>::open(w[u], x);
-                take<N>(m, s, x, k);
+                run.take(x, k);
             }
         }
         for (; v < v1; v += NT) {
             float x[N];
             Vec<T>::open(load16(z + v * N), x);
-            take<N>(m, s, x, k);
+            run.take(x, k);
         }
         if (part == a.parts - 1 && nv * N + tid < a.vocab) {
             const float x[1] = {Vec<T>::one(z[nv * N + tid])};
-            take<1>(m, s, x, k);
+            run.take(x, k);
         }
-        wg_join<NT>(m, s, k, lds);
+        wg_join<NT>(run, k, lds);
         if (tid == 0) {
-            a.stat[item] = make_float2(m, s);
+            a.stat[item] = RowStat{run.s, run.m, 0.0f};
             if (part == 0) a.token[row] = Vec<T>::one(z[a.target[row]]);
         }
     }
@@ -181,7 +195,7 @@ __global__ __launch_bounds__(NT) void row_stats_kernel(LogitRows a, PreferenceTe
 // --------------------------------------------------------------- token logp
 
 __global__ __launch_bounds__(256) void logp_kernel(LogitRows a, float* logp, float* lse) {
-    const float k = exponent_scale(a.scale);
+    const ExpScale k = a.k;
     for (int64_t row = blockIdx.x * 256ll + threadIdx.x; row < a.rows; row += gridDim.x * 256ll) {
         double l = 0.0, all = 0.0;
         if (has_token(a, row)) {
@@ -228,7 +242,7 @@ __device__ __forceinline__ PolicyRow policy_row(const LogitRows& a, const Policy
 template <int NT>
 __device__ void policy_summary(const LogitRows& a, const PolicyTerms& t, float* logp,
                                float* stats, double* lds) {
-    const float k = exponent_scale(a.scale);
+    const ExpScale k = a.k;
     double pg = 0.0, kl = 0.0, cl = 0.0;
     for (int64_t row = threadIdx.x; row < a.rows; row += NT) {
         PolicyRow p;
@@ -258,7 +272,7 @@ constexpr int64_t kGradSpan = 16384;
 // `tail`, the values behind the last vector.
 template <typename T, int NT>
 __device__ __forceinline__ void grad_span(const T* z, T* d, int64_t vocab, int64_t v0, int64_t v1,
-                                          bool tail, float k, const RowEnd& e, float cs, int64_t y,
+                                          bool tail, ExpScale k, const RowEnd& e, float cs, int64_t y,
                                           float token) {
     constexpr int N = Vec<T>::n, U = 4;
     const int tid = threadIdx.x;
@@ -291,7 +305,9 @@ __device__ __forceinline__ void grad_span(const T* z, T* d, int64_t vocab, int64
     const int64_t yv = y / N;
     const bool mine = yv < nv ? yv >= v0 && yv < v1 && (yv - v0) % NT == tid
                               : tail && y - nv * N == tid;
-    if (mine) d[y] = Vec<T>::pack(cs + f * term(token, e.r, k));
+    // (1 - p from the binary64 sum: next to p = 1 it is all that is left)
+    if (mine)
+        d[y] = Vec<T>::pack(cs * (float)((e.s - (double)term(token, e.r, k)) / e.s));
 }
 
 template <typename T, int NT>
@@ -314,7 +330,7 @@ __global__ __launch_bounds__(NT) void policy_grad_kernel(LogitRows a, PolicyTerm
         policy_summary<NT>(a, t, logp, stats, lds);
         return;
     }
-    const float k = exponent_scale(a.scale);
+    const ExpScale k = a.k;
     constexpr int N = Vec<T>::n;
     const int64_t nv = a.vocab / N, per = (nv + spans - 1) / spans;
     for (int64_t item = blockIdx.x - 1; item < a.rows * spans; item += gridDim.x - 1) {
@@ -348,7 +364,7 @@ template <int NT>
 __global__ __launch_bounds__(NT) void pair_kernel(LogitRows a, PreferenceTerms t, float* seq_logp) {
     __shared__ double lds[NT / 64];
     __shared__ double sum[2], count[2], slope;
-    const float k = exponent_scale(a.scale);
+    const ExpScale k = a.k;
     const int tid = threadIdx.x;
     const int64_t p = blockIdx.x;
     const double w = t.weight ? (double)t.weight[p] : 1.0 / (double)t.pairs;
@@ -430,7 +446,7 @@ __global__ __launch_bounds__(NT) void preference_grad_kernel(LogitRows a, Prefer
         preference_summary<NT>(t, stats, lds);
         return;
     }
-    const float k = exponent_scale(a.scale);
+    const ExpScale k = a.k;
     constexpr int N = Vec<T>::n;
     const int64_t nv = a.vocab / N, per = (nv + spans - 1) / spans;
     for (int64_t item = blockIdx.x - 1; item < a.rows * spans; item += gridDim.x - 1) {

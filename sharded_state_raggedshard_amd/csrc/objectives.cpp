@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <limits>
 #include <string>
 
 #include "objectives.hpp"
@@ -30,7 +31,7 @@ Scratch scratch_of(int64_t rows, int64_t vocab, int64_t n_seq) {
         at = align256(at + n);
         return p;
     };
-    s.stat = take(size_t(rows) * rs::stat_parts(rows, vocab) * sizeof(float2));
+    s.stat = take(size_t(rows) * rs::stat_parts(rows, vocab) * sizeof(rs::RowStat));
     s.token = take(size_t(rows) * sizeof(float));
     if (n_seq > 0) {
         s.mark = take(size_t(rows) * sizeof(int32_t));
@@ -69,8 +70,12 @@ rs_status fill_rows(const void* z, int32_t dtype, int64_t rows, int64_t vocab, i
     a.target = target;
     a.weight = nullptr;
     a.scale = 1.0 / temperature;
+    const double k = a.scale * 1.44269504088896340736;
+    a.k.hi = (float)k;
+    if ((double)a.k.hi > k) a.k.hi = std::nextafterf(a.k.hi, 0.0f);
+    a.k.lo = std::max((float)(k - (double)a.k.hi), std::numeric_limits<float>::min());
     a.parts = rs::stat_parts(rows, vocab);
-    a.stat = reinterpret_cast<float2*>(w + sc.stat);
+    a.stat = reinterpret_cast<rs::RowStat*>(w + sc.stat);
     a.token = reinterpret_cast<float*>(w + sc.token);
     return RS_OK;
 }

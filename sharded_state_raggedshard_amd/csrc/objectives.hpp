@@ -10,6 +10,18 @@ namespace rs {
 
 constexpr int64_t kMaxVocab = int64_t(1) << 24;
 
+// log2(e) / temperature as hi + lo, hi rounded towards 0 and lo > 0 (so that
+// -inf times either is -inf).
+struct ExpScale {
+    float hi, lo;
+};
+
+// Maximum and sum of exponentials of (a part of) a row.
+struct RowStat {
+    double s;
+    float m, unused;
+};
+
 // Rows of logits and, per row, what the kernels keep of them in scratch.
 struct LogitRows {
     const void* z;
@@ -18,9 +30,10 @@ struct LogitRows {
     const int64_t* target;
     const float* weight;  // per row (policy) or nullptr
     double scale;         // 1 / temperature
+    ExpScale k;
     // scratch: `parts` (max, sum) pairs and the token's logit per row
     int32_t parts;
-    float2* stat;
+    RowStat* stat;
     float* token;
 };
 

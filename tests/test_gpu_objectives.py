@@ -6,8 +6,9 @@ Tolerances, from the arithmetic of the kernels (u = 2^-24, half a step of
 binary32; R = max |z - max z| / T of the row):
   an exponential: exponent scale, difference and product each rounded once
       on values of size R, and one ulp of exp2: (3 R + 3) u of its value;
-  the row sum: that, and binary32 additions, fewer than V / 64 + 40 in a
-      chain: d_s = (3 R + 3 + V / 64 + 40) u;
+  the row sum: that, four binary32 additions in a chain and binary64 ones,
+      up to 8 rescalings by an exponential that are not by 1:
+      d_s = (3 R + 3 + 4 + 8 (3 R + 3)) u;
   logp: d_l = d_s, and u |logp| for the output;
   dloss/dlogp: |c'(l)| d_l with c' bounded from its formula, and u |c|;
   a gradient value: c p off by (d_s + (3 R + 3) u + 4 u) |c| p + dc p, the
@@ -47,13 +48,12 @@ def np64(t):
 
 def row_bounds(z, temperature):
     """(R, d_s) per row."""
-    vocab = z.shape[1]
     with np.errstate(all="ignore"):
         top = np.max(np.where(np.isfinite(z), z, -1e300), axis=1)
         # values far below the top count as 0 on either side
         fall = np.where(np.isfinite(z), top[:, None] - z, 0.0) / temperature
         R = np.minimum(fall.max(axis=1), 90.0)
-    return R, (3 * R + 3 + vocab / 64 + 40) * U
+    return R, (9 * (3 * R + 3) + 4) * U
 
 
 def check_gradient(got, exp, z, target, temperature, dcoef, dtype, what):
