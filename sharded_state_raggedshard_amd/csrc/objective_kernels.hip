@@ -6,8 +6,10 @@
 // is exp2((z - m) k), k = log2(e) / T in two binary32 pieces: one alone
 // would shift every term the same way (up to 2^-24 |z - m| / T, so the
 // row's logarithm with them), where the product's own rounding averages out.
-// (Folding m into one fused multiply-add, z k - m k, saves an instruction
-// but overflows on masks of the type's lowest value.)
+// (Folding m into one fused multiply-add, z k - m k, saves two instructions
+// of eleven a value, measured no faster, as memory bounds these kernels; it
+// rounds at the size of m k and overflows on masks of the type's lowest
+// value.)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -22,102 +24,102 @@ namespace {
 
 using namespace rows;
 
-// What is subtracted for maximum m; 0 while nothing but -inf was seen, so
-// that -inf values give exp2(-inf) = 0.
-__device__ __forceinline__ float reference(float m) { return m == kNegInf ? 0.0f : m; }
-
-__device__ __forceinline__ float term(float x, float r, ExpScale k) {
-    const float d = x - r;
+// exp((x - m) / T)
+__device__ __forceinline__ float term(float x, float m, ExpScale k) {
+    const float d = x - m;
     return exp2_fast(__builtin_fmaf(d, k.hi, d * k.lo));
 }
 
-// Running maximum and sum.  The sum is binary64: where one term is nearly
-// the whole row, as a trained model's are, a binary32 sum would round away
-// the rest that 1 - p is made of.  It takes N terms at a time, added up in
-// binary32.
-struct Running {
+// Maximum and sum, of a thread's share of a row, a part of it or a row.  The
+// sum is binary64: where one term is nearly the whole row, as a trained
+// model's are, a binary32 sum would round away the rest that 1 - p is made
+// of.  It takes the C values of a call at once, added up in binary32 in four
+// chains.
+struct MaxSum {
     float m = kNegInf;
     double s = 0.0;
 
-    template <int N>
-    __device__ __forceinline__ void take(const float (&x)[N], ExpScale k) {
+    template <int C>
+    __device__ __forceinline__ void take(const float (&x)[C], ExpScale k) {
         float v = x[0];
 #pragma unroll
-        for (int i = 1; i < N; ++i) v = fmaxf(v, x[i]);
-        const float M = fmaxf(m, v), r = reference(M);
-        float a = 0.0f, b = 0.0f;
+        for (int i = 1; i < C; ++i) v = fmaxf(v, x[i]);
+        const float M = fmaxf(m, v);
+        const float r = M == kNegInf ? 0.0f : M;  // -inf - 0 gives exp2(-inf) = 0
+        float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            a += term(x[i], r, k);
-            if (i + 1 < N) b += term(x[i + 1], r, k);
-        }
-        s = __builtin_fma(s, (double)term(m, r, k), (double)(a + b));
+        for (int i = 0; i < C; ++i) a[i % 4] += term(x[i], r, k);
+        s = __builtin_fma(s, (double)term(m, r, k), (double)((a[0] + a[1]) + (a[2] + a[3])));
         m = M;
     }
 
     __device__ __forceinline__ void join(float m2, double s2, ExpScale k) {
-        const float M = fmaxf(m, m2), r = reference(M);
+        const float M = fmaxf(m, m2);
+        const float r = M == kNegInf ? 0.0f : M;
         s = s * (double)term(m, r, k) + s2 * (double)term(m2, r, k);
         m = M;
     }
 };
 
-// The Running of a whole workgroup, in a fixed order; valid in every thread.
-// lds: 2 doubles per wave.
+// LDS of wg_join.
 template <int NT>
-__device__ __forceinline__ void wg_join(Running& x, ExpScale k, double* lds) {
+struct JoinLds {
+    double s[NT / 64];
+    float m[NT / 64];
+};
+
+// The MaxSum of the whole workgroup, in a fixed order; valid in every
+// thread.  Ends with a barrier.
+template <int NT>
+__device__ __forceinline__ MaxSum wg_join(MaxSum x, ExpScale k, JoinLds<NT>& lds) {
     float M = x.m;
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
-    x.s *= (double)term(x.m, reference(M), k);
+    x.s *= (double)term(x.m, M == kNegInf ? 0.0f : M, k);
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) x.s += __shfl_xor(x.s, off, 64);
     x.m = M;
-    if (NT == 64) return;
-    const int wave = threadIdx.x >> 6;
+    if (NT == 64) return x;
     if ((threadIdx.x & 63) == 0) {
-        lds[2 * wave] = x.s;
-        lds[2 * wave + 1] = (double)x.m;
+        lds.s[threadIdx.x >> 6] = x.s;
+        lds.m[threadIdx.x >> 6] = M;
     }
     __syncthreads();
-    M = kNegInf;
 #pragma unroll
-    for (int w = 0; w < NT / 64; ++w) M = fmaxf(M, (float)lds[2 * w + 1]);
-    double S = 0.0;
+    for (int w = 0; w < NT / 64; ++w) M = fmaxf(M, lds.m[w]);
+    x.m = M;
+    x.s = 0.0;
 #pragma unroll
     for (int w = 0; w < NT / 64; ++w)
-        S += lds[2 * w] * (double)term((float)lds[2 * w + 1], reference(M), k);
+        x.s += lds.s[w] * (double)term(lds.m[w], M == kNegInf ? 0.0f : M, k);
     __syncthreads();
-    x.m = M;
-    x.s = S;
+    return x;
 }
 
 // What the statistics of a row come to.
 struct RowEnd {
-    float m, r;    // maximum; what the exponentials subtract
-    float inv;     // 1 / sum
+    float m;
     double s;
     double lse_m;  // log sum exp((z - m) / T)
     bool empty;    // nothing but -inf
 };
 
-__device__ __forceinline__ RowEnd row_end(const Running& x) {
+__device__ __forceinline__ RowEnd row_end(const MaxSum& x) {
     RowEnd e;
     e.m = x.m;
     e.s = x.s;
     e.empty = x.m == kNegInf && x.s == 0.0;
-    e.r = reference(x.m);
-    e.inv = (float)(1.0 / x.s);
     e.lse_m = e.empty ? 0.0 : log(x.s);
     return e;
 }
 
 __device__ __forceinline__ RowEnd row_of(const LogitRows& a, int64_t row, ExpScale k) {
     const RowStat* p = a.stat + row * a.parts;
-    Running x;
-    x.m = p[0].m;
-    x.s = p[0].s;
-    for (int i = 1; i < a.parts; ++i) x.join(p[i].m, p[i].s, k);
+    MaxSum x{p[0].m, p[0].s};
+    for (int i = 1; i < a.parts; ++i) {
+        const RowStat q = p[i];
+        x.join(q.m, q.s, k);
+    }
     return row_end(x);
 }
 
@@ -132,25 +134,105 @@ __device__ __forceinline__ bool has_token(const LogitRows& a, int64_t row) {
 
 // --------------------------------------------------------- row statistics
 
+// A row of `vocab` values in 16-byte pieces at 16-byte addresses: rows of an
+// odd length start anywhere, and pieces across 16-byte lines cost a quarter
+// of the bandwidth (6001 x 32003 bf16: 85 us, x 32000: 66 us).  `head` values
+// lie in front of the pieces; `edges` values, fewer than 2 N, in front of and
+// behind them, one each for the first threads.
+template <typename T>
+struct Pieces {
+    static constexpr int N = Vec<T>::n;
+    int head, n, edges;
+    __device__ __forceinline__ Pieces(const T* row, int64_t vocab) {
+        const int to_line = (int)((16u - (unsigned)(reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / (int)sizeof(T);
+        head = to_line < (int)vocab ? to_line : (int)vocab;
+        n = ((int)vocab - head) / N;
+        edges = (int)vocab - n * N;
+    }
+    __device__ __forceinline__ int edge(int i) const { return i < head ? i : n * N + i; }
+    // piece of value y, -1 for an edge
+    __device__ __forceinline__ int piece(int y) const {
+        return y >= head && (y - head) / N < n ? (y - head) / N : -1;
+    }
+};
+
+// A part of a row: pieces [v0, v1) and, if `ends`, the edges.  Parts meet at
+// 128-byte lines: a line that two workgroups write, on two L2 caches, costs
+// a read and a merge (gradients of 4470 of 6697 rows x 128256 bf16 in parts
+// of 32 to 50 KB: 540 to 560 us with lines shared, 505 us without).
+struct Part {
+    int v0, v1;
+    bool ends;
+};
+
+template <typename T>
+__device__ __forceinline__ Part part_of(const T* row, const Pieces<T>& ps, int part, int parts) {
+    if (parts == 1) return Part{0, ps.n, true};
+    const int shift = (int)(reinterpret_cast<uintptr_t>(row + ps.head) >> 4) & 7;
+    const int per = ((ps.n + shift + parts - 1) / parts + 7) / 8 * 8;
+    const int a = part * per - shift, b = a + per;
+    return Part{a < 0 ? 0 : a < ps.n ? a : ps.n, b < ps.n ? b : ps.n, part == parts - 1};
+}
+
+// Statistics of a part of a row, by the whole workgroup: U loads a thread in
+// flight (the last ones padded with -inf).  ONCE: not read again soon.
+template <typename T, int NT, bool ONCE>
+__device__ __forceinline__ void take_part(MaxSum& run, const T* z, const Pieces<T>& ps, Part part,
+                                          ExpScale k) {
+    constexpr int N = Vec<T>::n, U = 4;
+    const int tid = threadIdx.x;
+    const T* base = z + ps.head;
+    for (int v = part.v0 + tid; v < part.v1; v += U * NT) {
+        u32x4 w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            w[u] = Vec<T>::lowest();
+            const int at = v + u * NT;
+            if (at < part.v1) w[u] = ONCE ? load16_once(base + at * N) : load16(base + at * N);
+        }
+        float x[U * N];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float y[N];
+            Vec<T>::open(w[u], y);
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[u * N + i] = y[i];
+        }
+        run.take(x, k);
+    }
+    if (part.ends && tid < ps.edges) {
+        const float x[1] = {Vec<T>::one(z[ps.edge(tid)])};
+        run.take(x, k);
+    }
+}
+
 enum { MARK_OUTSIDE = 0, MARK_ZERO = 1, MARK_TOKEN = 2 };
 
-// One workgroup per part of a row: its maximum and sum in one pass, four
-// 16-byte loads a thread in flight.  For the preference loss it also marks
-// the rows (outside every sequence, without a token, with one).
-template <typename T, int NT, bool PREF>
-__global__ __launch_bounds__(NT) void row_stats_kernel(LogitRows a, PreferenceTerms t) {
-    constexpr int N = Vec<T>::n, U = 4;
-    __shared__ double lds[2 * (NT / 64)];
+// What row_stats_kernel does beside the statistics: nothing; writes logp (and
+// lse) of whole rows; marks rows for the preference loss (outside every
+// sequence, without a token, with one).
+enum { STATS_ONLY = 0, STATS_LOGP = 1, STATS_MARK = 2 };
+
+__device__ __forceinline__ void write_logp(const LogitRows& a, int64_t row, const RowEnd& e,
+                                           float token, float* logp, float* lse) {
+    logp[row] = e.empty ? 0.0f : (float)logp_of(e, token, a.scale);
+    if (lse) lse[row] = e.empty ? 0.0f : (float)((double)e.m * a.scale + e.lse_m);
+}
+
+// One workgroup per part of a row: its maximum and sum in one pass over the
+// logits.  Bound by HBM: 6.5 TB/s on 8192 x 128256 bf16 (322 us).
+template <typename T, int NT, int MODE>
+__global__ __launch_bounds__(NT) void row_stats_kernel(LogitRows a, PreferenceTerms t, float* logp,
+                                                       float* lse) {
+    __shared__ JoinLds<NT> lds;
     const int tid = threadIdx.x;
     const ExpScale k = a.k;
     const int64_t items = a.rows * a.parts;
-    const int64_t nv = a.vocab / N;
-    const int64_t per = (nv + a.parts - 1) / a.parts;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int64_t row = item / a.parts;
+        const int64_t row = a.parts == 1 ? item : item / a.parts;
         const int part = (int)(item - row * a.parts);
         bool live = has_token(a, row);
-        if (PREF) {
+        if (MODE == STATS_MARK) {
             const int64_t seq = sequence_of(t.start, 2 * t.pairs, row);
             const bool inside = seq < 2 * t.pairs && row >= t.start[0];
             if (inside && t.weight)
@@ -159,55 +241,56 @@ __global__ __launch_bounds__(NT) void row_stats_kernel(LogitRows a, PreferenceTe
             if (part == 0 && tid == 0)
                 t.mark[row] = !inside ? MARK_OUTSIDE : live ? MARK_TOKEN : MARK_ZERO;
         }
-        if (!live) continue;
-        const T* z = static_cast<const T*>(a.z) + row * a.ld;
-        Running run;
-        const int64_t v0 = part * per, v1 = min(nv, v0 + per);
-        int64_t v = v0 + tid;
-        for (; v + (U - 1) * NT < v1; v += U * NT) {
-            u32x4 w[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) w[u] = load16(z + (v + u * NT) * N);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float x[N];
-                Vec<T>::open(w[u], x);
-                run.take(x, k);
+        if (!live) {
+            if (MODE == STATS_LOGP && tid == 0) {
+                logp[row] = 0.0f;
+                if (lse) lse[row] = 0.0f;
             }
+            continue;
         }
-        for (; v < v1; v += NT) {
-            float x[N];
-            Vec<T>::open(load16(z + v * N), x);
-            run.take(x, k);
-        }
-        if (part == a.parts - 1 && nv * N + tid < a.vocab) {
-            const float x[1] = {Vec<T>::one(z[nv * N + tid])};
-            run.take(x, k);
-        }
-        wg_join<NT>(run, k, lds);
-        if (tid == 0) {
+        const T* z = static_cast<const T*>(a.z) + row * a.ld;
+        const float token = Vec<T>::one(z[a.target[row]]);
+        const Pieces<T> ps(z, a.vocab);
+        MaxSum run;
+        if (MODE == STATS_MARK && row >= t.kept_from)
+            take_part<T, NT, false>(run, z, ps, part_of(z, ps, part, a.parts), k);
+        else
+            take_part<T, NT, true>(run, z, ps, part_of(z, ps, part, a.parts), k);
+        run = wg_join<NT>(run, k, lds);
+        if (tid != 0) continue;
+        if (MODE == STATS_LOGP) {
+            write_logp(a, row, row_end(run), token, logp, lse);
+        } else {
             a.stat[item] = RowStat{run.s, run.m, 0.0f};
-            if (part == 0) a.token[row] = Vec<T>::one(z[a.target[row]]);
+            if (part == 0) a.token[row] = token;
         }
     }
 }
 
 // --------------------------------------------------------------- token logp
 
+// Joins the parts of split rows (parts: a power of two up to 32), a lane a
+// part.
+__device__ __forceinline__ MaxSum join_parts(const LogitRows& a, int64_t row, int part) {
+    const RowStat p = a.stat[row * a.parts + part];
+    MaxSum x{p.m, p.s};
+    for (int off = 1; off < a.parts; off <<= 1)
+        x.join(__shfl_xor(x.m, off, 64), __shfl_xor(x.s, off, 64), a.k);
+    return x;
+}
+
 __global__ __launch_bounds__(256) void logp_kernel(LogitRows a, float* logp, float* lse) {
-    const ExpScale k = a.k;
-    for (int64_t row = blockIdx.x * 256ll + threadIdx.x; row < a.rows; row += gridDim.x * 256ll) {
-        double l = 0.0, all = 0.0;
-        if (has_token(a, row)) {
-            const RowEnd e = row_of(a, row, k);
-            if (!e.empty) {
-                l = logp_of(e, a.token[row], a.scale);
-                all = (double)e.m * a.scale + e.lse_m;
-            }
-        }
-        logp[row] = (float)l;
-        if (lse) lse[row] = (float)all;
+    const int64_t at = blockIdx.x * 256ll + threadIdx.x, row = at / a.parts;
+    const int part = (int)(at - row * a.parts);
+    if (row >= a.rows) return;
+    RowEnd e;
+    e.empty = true;
+    float token = 0.0f;
+    if (has_token(a, row)) {
+        token = a.token[row];
+        e = row_end(join_parts(a, row, part));
     }
+    if (part == 0) write_logp(a, row, e, token, logp, lse);
 }
 
 // -------------------------------------------------------------- policy loss
@@ -238,128 +321,226 @@ __device__ __forceinline__ PolicyRow policy_row(const LogitRows& a, const Policy
     return p;
 }
 
-// Per-row outputs and the loss sums, by one workgroup in a fixed order.
+// Sums of n triples, by one workgroup in a fixed order; valid in thread 0.
 template <int NT>
-__device__ void policy_summary(const LogitRows& a, const PolicyTerms& t, float* logp,
-                               float* stats, double* lds) {
-    const ExpScale k = a.k;
-    double pg = 0.0, kl = 0.0, cl = 0.0;
-    for (int64_t row = threadIdx.x; row < a.rows; row += NT) {
-        PolicyRow p;
-        if (has_token(a, row)) p = policy_row(a, t, row, row_of(a, row, k), a.token[row]);
-        pg += p.pg;
-        kl += p.kl;
-        cl += p.clipped;
-        if (logp) logp[row] = (float)p.logp;
-    }
-    pg = wg_sum<NT>(pg, lds);
-    kl = wg_sum<NT>(kl, lds);
-    cl = wg_sum<NT>(cl, lds);
-    if (threadIdx.x == 0) {
-        stats[0] = (float)(pg + (t.ref_logp ? t.kl_coef * kl : 0.0));
-        stats[1] = (float)pg;
-        stats[2] = (float)kl;
-        stats[3] = (float)cl;
-    }
+__device__ __forceinline__ void sum_terms(const double* terms, int64_t n, double (&sum)[3],
+                                          double* lds) {
+    double x[3] = {0.0, 0.0, 0.0};
+    for (int64_t i = threadIdx.x; i < n; i += NT)
+        for (int j = 0; j < 3; ++j) x[j] += terms[3 * i + j];
+    for (int j = 0; j < 3; ++j) sum[j] = wg_sum<NT>(x[j], lds);
+}
+
+__device__ __forceinline__ void policy_stats(const PolicyTerms& t, const double (&sum)[3],
+                                             float* stats) {
+    stats[0] = (float)(sum[0] + (t.ref_logp ? t.kl_coef * sum[1] : 0.0));
+    for (int j = 0; j < 3; ++j) stats[1 + j] = (float)sum[j];
 }
 
 // ----------------------------------------------------------- logits gradient
 
-// Elements of a row that one workgroup of the gradient kernels writes.
-constexpr int64_t kGradSpan = 16384;
+// What the gradient of a row, cs ([i = y] - p_i), takes: f = -cs / s and the
+// token's own value cs (1 - p), where 1 - p comes from the binary64 sum, as
+// next to p = 1 it is all that is left.
+__device__ __forceinline__ GradRow grad_row(const RowEnd& e, double cs, int64_t y, float token,
+                                            ExpScale k) {
+    GradRow g;
+    g.m = e.m;
+    g.f = (float)(-cs / e.s);
+    g.own = (float)(cs * ((e.s - (double)term(token, e.m, k)) / e.s));
+    g.y = (int32_t)y;
+    return g;
+}
 
-// d[i] = cs ([i = token] - p_i) for the vectors [v0, v1) of a row and, with
-// `tail`, the values behind the last vector.
+__device__ __forceinline__ float grad_one(const GradRow& g, float x, ExpScale k) {
+    return g.f * term(x, g.m, k);
+}
+
+// 16 bytes of a row's gradient.
+template <typename T>
+__device__ __forceinline__ u32x4 grad16(const GradRow& g, const u32x4& w, ExpScale k) {
+    constexpr int N = Vec<T>::n;
+    float x[N];
+    Vec<T>::open(w, x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = grad_one(g, x[i], k);
+    return Vec<T>::close(x);
+}
+
+// The gradient of a part of a row.
 template <typename T, int NT>
-__device__ __forceinline__ void grad_span(const T* z, T* d, int64_t vocab, int64_t v0, int64_t v1,
-                                          bool tail, ExpScale k, const RowEnd& e, float cs, int64_t y,
-                                          float token) {
+__device__ __forceinline__ void grad_part(const T* z, T* d, const Pieces<T>& ps, Part part,
+                                          ExpScale k, const GradRow& g) {
     constexpr int N = Vec<T>::n, U = 4;
     const int tid = threadIdx.x;
-    const float f = -cs * e.inv;
-    int64_t v = v0 + tid;
-    for (; v + (U - 1) * NT < v1; v += U * NT) {
+    const T* from = z + ps.head;
+    T* to = d + ps.head;
+    for (int v = part.v0 + tid; v < part.v1; v += U * NT) {
         u32x4 w[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) w[u] = load16(z + (v + u * NT) * N);
+        for (int u = 0; u < U; ++u)
+            if (v + u * NT < part.v1) w[u] = load16_once(from + (v + u * NT) * N);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float x[N];
-            Vec<T>::open(w[u], x);
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = f * term(x[i], e.r, k);
-            store16(d + (v + u * NT) * N, Vec<T>::close(x));
-        }
+        for (int u = 0; u < U; ++u)
+            if (v + u * NT < part.v1) store16(to + (v + u * NT) * N, grad16<T>(g, w[u], k));
     }
-    for (; v < v1; v += NT) {
-        float x[N];
-        Vec<T>::open(load16(z + v * N), x);
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = f * term(x[i], e.r, k);
-        store16(d + v * N, Vec<T>::close(x));
-    }
-    const int64_t nv = vocab / N, last = nv * N + tid;
-    if (tail && last < vocab)
-        d[last] = Vec<T>::pack(f * term(Vec<T>::one(z[last]), e.r, k));
+    if (part.ends && tid < ps.edges)
+        d[ps.edge(tid)] = Vec<T>::pack(grad_one(g, Vec<T>::one(z[ps.edge(tid)]), k));
     // the token's own value, by the thread that has just written its place
-    const int64_t yv = y / N;
-    const bool mine = yv < nv ? yv >= v0 && yv < v1 && (yv - v0) % NT == tid
-                              : tail && y - nv * N == tid;
-    // (1 - p from the binary64 sum: next to p = 1 it is all that is left)
-    if (mine)
-        d[y] = Vec<T>::pack(cs * (float)((e.s - (double)term(token, e.r, k)) / e.s));
+    const int yv = ps.piece(g.y);
+    const bool mine = yv >= 0 ? yv >= part.v0 && yv < part.v1 && (yv - part.v0) % NT == tid
+                              : part.ends && tid < ps.edges && ps.edge(tid) == g.y;
+    if (mine) d[g.y] = Vec<T>::pack(g.own);
 }
 
 template <typename T, int NT>
-__device__ __forceinline__ void zero_span(T* d, int64_t vocab, int64_t v0, int64_t v1, bool tail) {
-    constexpr int N = Vec<T>::n;
+__device__ __forceinline__ void zero_part(T* d, const Pieces<T>& ps, Part part) {
     const u32x4 z = {0u, 0u, 0u, 0u};
-    for (int64_t v = v0 + threadIdx.x; v < v1; v += NT) store16(d + v * N, z);
-    const int64_t last = vocab / N * N + threadIdx.x;
-    if (tail && last < vocab) d[last] = T(0);
+    for (int v = part.v0 + threadIdx.x; v < part.v1; v += NT)
+        store16(d + ps.head + v * Vec<T>::n, z);
+    if (part.ends && (int)threadIdx.x < ps.edges) d[ps.edge(threadIdx.x)] = T(0);
 }
 
-// Workgroup 0 sums the losses; the others each write a span of a row.
+// ------------------------------------------------------- policy loss, split
+
+// Few long rows: row_stats_kernel over parts, then this kernel, in which
+// workgroup 0 computes the rows' outputs and the loss sums and every other
+// one writes a part of a row's gradient.
 template <typename T, int NT>
 __global__ __launch_bounds__(NT) void policy_grad_kernel(LogitRows a, PolicyTerms t, T* d,
-                                                         int64_t ldd, int64_t spans, float* logp,
+                                                         int64_t ldd, int spans, float* logp,
                                                          float* stats) {
     __shared__ double lds[NT / 64];
-    __shared__ float coef;
+    __shared__ GradRow g;
+    const int tid = threadIdx.x;
+    const ExpScale k = a.k;
     if (blockIdx.x == 0) {
-        policy_summary<NT>(a, t, logp, stats, lds);
+        double pg = 0.0, kl = 0.0, cl = 0.0;
+        const int part = tid % a.parts;
+        for (int64_t row = tid / a.parts; row < a.rows; row += NT / a.parts) {
+            PolicyRow p;
+            if (has_token(a, row)) {
+                const float token = a.token[row];
+                const RowEnd e = row_end(join_parts(a, row, part));
+                if (part == 0) p = policy_row(a, t, row, e, token);
+            }
+            pg += p.pg;
+            kl += p.kl;
+            cl += p.clipped;
+            if (part == 0 && logp) logp[row] = (float)p.logp;
+        }
+        const double sum[3] = {wg_sum<NT>(pg, lds), wg_sum<NT>(kl, lds), wg_sum<NT>(cl, lds)};
+        if (tid == 0) policy_stats(t, sum, stats);
         return;
     }
-    const ExpScale k = a.k;
-    constexpr int N = Vec<T>::n;
-    const int64_t nv = a.vocab / N, per = (nv + spans - 1) / spans;
-    for (int64_t item = blockIdx.x - 1; item < a.rows * spans; item += gridDim.x - 1) {
-        const int64_t row = item / spans, part = item - row * spans;
-        const int64_t v0 = part * per, v1 = min(nv, v0 + per);
-        T* to = d + row * ldd;
-        RowEnd e;
-        bool live = has_token(a, row);
-        if (live) {
-            e = row_of(a, row, k);
-            live = !e.empty;
+    const int64_t item = blockIdx.x - 1, row = item / spans;
+    const int span = (int)(item - row * spans);
+    const T* z = static_cast<const T*>(a.z) + row * a.ld;
+    T* to = d + row * ldd;
+    const Pieces<T> ps(z, a.vocab);
+    const Part part = part_of(z, ps, span, spans);
+    bool live = has_token(a, row);
+    if (live) {
+        const RowEnd e = row_end(join_parts(a, row, tid % a.parts));
+        live = !e.empty;
+        if (live && tid == 0) {
+            const float token = a.token[row];
+            g = grad_row(e, policy_row(a, t, row, e, token).coef * a.scale, a.target[row], token, k);
         }
-        if (!live) {
-            zero_span<T, NT>(to, a.vocab, v0, v1, part == spans - 1);
-            continue;
-        }
-        const float token = a.token[row];
-        __syncthreads();
-        if (threadIdx.x == 0) coef = (float)(policy_row(a, t, row, e, token).coef * a.scale);
-        __syncthreads();
-        grad_span<T, NT>(static_cast<const T*>(a.z) + row * a.ld, to, a.vocab, v0, v1,
-                         part == spans - 1, k, e, coef, a.target[row], token);
     }
+    __syncthreads();
+    if (live)
+        grad_part<T, NT>(z, to, ps, part, k, g);
+    else
+        zero_part<T, NT>(to, ps, part);
+}
+
+// ------------------------------------------------------ policy loss, by row
+
+// One workgroup per row: statistics, coefficient and gradient.  The first
+// kHeld pieces of every thread stay in its registers in between; the rest is
+// read again, out of the cache that holds it if few enough rows are under
+// way.  Four waves a SIMD (128 registers) is what 12 held pieces leave: 2
+// workgroups of 512 a unit, so that one reads while the other writes.
+//
+// 6144 of 8192 rows x 128256 bf16, in us: two kernels over all rows 981;
+// nothing held 793 (512 threads); 12 held 743; with the gradient stored past
+// the caches 710, and held pieces read past them 698 (5.3 TB/s of the
+// 3.68 GB it cannot do without).  16 held (spills) 747, 8 held 750.  Holding
+// all of a row in 1024 threads and loading the next row while storing took
+// 920: four waves a SIMD in step leave the memory idle while they sum.
+constexpr int kHeld = 12;
+
+template <typename T, int NT>
+__global__ __launch_bounds__(NT, 4) void policy_row_kernel(LogitRows a, PolicyTerms t, int64_t row0,
+                                                           T* d, int64_t ldd, float* logp) {
+    constexpr int N = Vec<T>::n;
+    __shared__ JoinLds<NT> lds;
+    __shared__ GradRow g;
+    const ExpScale k = a.k;
+    const int tid = threadIdx.x;
+    const int64_t row = row0 + blockIdx.x;
+    const T* z = static_cast<const T*>(a.z) + row * a.ld;
+    T* to = d + row * ldd;
+    const Pieces<T> ps(z, a.vocab);
+    RowEnd e;
+    e.empty = true;
+    u32x4 w[kHeld];
+    if (has_token(a, row)) {
+        const float token = Vec<T>::one(z[a.target[row]]);
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+            if (j * NT + tid < ps.n) w[j] = load16_once(z + ps.head + (j * NT + tid) * N);
+        MaxSum run;
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            if (j * NT + tid < ps.n) {
+                float x[N];
+                Vec<T>::open(w[j], x);
+                run.take(x, k);
+            }
+        }
+        take_part<T, NT, false>(run, z, ps, Part{kHeld * NT, ps.n, true}, k);
+        e = row_end(wg_join<NT>(run, k, lds));
+        if (tid == 0 && !e.empty) {
+            const PolicyRow p = policy_row(a, t, row, e, token);
+            g = grad_row(e, p.coef * a.scale, a.target[row], token, k);
+            t.terms[3 * row] = p.pg;
+            t.terms[3 * row + 1] = p.kl;
+            t.terms[3 * row + 2] = p.clipped;
+            if (logp) logp[row] = (float)p.logp;
+        }
+        __syncthreads();
+    }
+    if (e.empty) {
+        if (tid == 0) {
+            for (int i = 0; i < 3; ++i) t.terms[3 * row + i] = 0.0;
+            if (logp) logp[row] = 0.0f;
+        }
+        if (d) zero_part<T, NT>(to, ps, Part{0, ps.n, true});
+        return;
+    }
+    if (!d) return;
+    const GradRow gr = g;
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+        if (j * NT + tid < ps.n) store16(to + ps.head + (j * NT + tid) * N, grad16<T>(gr, w[j], k));
+    const int yv = ps.piece(gr.y);
+    if (yv >= 0 && yv < kHeld * NT && yv % NT == tid) to[gr.y] = Vec<T>::pack(gr.own);
+    grad_part<T, NT>(z, to, ps, Part{kHeld * NT, ps.n, true}, k, gr);
+}
+
+__global__ __launch_bounds__(1024) void policy_sum_kernel(PolicyTerms t, int64_t rows, float* stats) {
+    __shared__ double lds[16];
+    double sum[3];
+    sum_terms<1024>(t.terms, rows, sum, lds);
+    if (threadIdx.x == 0) policy_stats(t, sum, stats);
 }
 
 // ---------------------------------------------------------- preference loss
 
 // One workgroup per pair: its sequences' log-probabilities, its loss and
-// the coefficient dloss / dlogp / T of its rows.
+// what its rows' gradients take.
 template <int NT>
 __global__ __launch_bounds__(NT) void pair_kernel(LogitRows a, PreferenceTerms t, float* seq_logp) {
     __shared__ double lds[NT / 64];
@@ -422,116 +603,181 @@ __global__ __launch_bounds__(NT) void pair_kernel(LogitRows a, PreferenceTerms t
         const int64_t q = p + side * t.pairs;
         const int64_t r0 = min(max(t.start[q], int64_t(0)), a.rows);
         const int64_t r1 = min(max(t.start[q + 1], r0), a.rows);
-        const float c = (float)((side ? -slope : slope) / count[side]);
-        for (int64_t row = r0 + tid; row < r1; row += NT) t.coef[row] = c;
+        const double cs = (side ? -slope : slope) / count[side];
+        for (int64_t row = r0 + tid; row < r1; row += NT)
+            if (t.mark[row] == MARK_TOKEN)
+                t.grad[row] = grad_row(row_of(a, row, k), cs, a.target[row], a.token[row], k);
     }
 }
 
 template <int NT>
 __device__ void preference_summary(const PreferenceTerms& t, float* stats, double* lds) {
-    for (int i = 0; i < 3; ++i) {
-        double x = 0.0;
-        for (int64_t p = threadIdx.x; p < t.pairs; p += NT) x += t.terms[3 * p + i];
-        x = wg_sum<NT>(x, lds);
-        if (threadIdx.x == 0) stats[i] = (float)x;
-    }
+    double sum[3];
+    sum_terms<NT>(t.terms, t.pairs, sum, lds);
+    if (threadIdx.x == 0)
+        for (int i = 0; i < 3; ++i) stats[i] = (float)sum[i];
 }
 
+// Workgroup 0 sums the losses; the others each write a part of a row, the
+// last rows first: the statistics have left those in the memory-side cache.
 template <typename T, int NT>
 __global__ __launch_bounds__(NT) void preference_grad_kernel(LogitRows a, PreferenceTerms t, T* d,
-                                                             int64_t ldd, int64_t spans,
-                                                             float* stats) {
+                                                             int64_t ldd, int spans, float* stats) {
     __shared__ double lds[NT / 64];
     if (blockIdx.x == 0) {
         preference_summary<NT>(t, stats, lds);
         return;
     }
-    const ExpScale k = a.k;
-    constexpr int N = Vec<T>::n;
-    const int64_t nv = a.vocab / N, per = (nv + spans - 1) / spans;
-    for (int64_t item = blockIdx.x - 1; item < a.rows * spans; item += gridDim.x - 1) {
-        const int64_t row = item / spans, part = item - row * spans;
-        const int64_t v0 = part * per, v1 = min(nv, v0 + per);
+    const int64_t items = a.rows * spans;
+    for (int64_t i = blockIdx.x - 1; i < items; i += gridDim.x - 1) {
+        const int64_t item = items - 1 - i, row = item / spans;
         const int mark = t.mark[row];
         if (mark == MARK_OUTSIDE) continue;
+        const T* z = static_cast<const T*>(a.z) + row * a.ld;
         T* to = d + row * ldd;
-        if (mark == MARK_ZERO) {
-            zero_span<T, NT>(to, a.vocab, v0, v1, part == spans - 1);
-            continue;
-        }
-        const RowEnd e = row_of(a, row, k);
-        grad_span<T, NT>(static_cast<const T*>(a.z) + row * a.ld, to, a.vocab, v0, v1,
-                         part == spans - 1, k, e, t.coef[row], a.target[row], a.token[row]);
+        const Pieces<T> ps(z, a.vocab);
+        const Part part = part_of(z, ps, (int)(item - row * spans), spans);
+        if (mark == MARK_ZERO)
+            zero_part<T, NT>(to, ps, part);
+        else
+            grad_part<T, NT>(z, to, ps, part, a.k, t.grad[row]);
     }
 }
 
-// Rows up to this many values take one wave each.
-constexpr int64_t kWaveRow = 2048;
+// Rows of up to this many bytes take one wave each in the statistics.
+constexpr int64_t kWaveRow = 16 << 10;
 
-template <bool PREF>
-hipError_t launch_stats(const LogitRows& a, const PreferenceTerms& t, hipStream_t s) {
+int64_t row_bytes(const LogitRows& a) { return a.vocab * (a.f32 ? 4 : 2); }
+
+template <int NT, int MODE>
+hipError_t launch_stats_nt(const LogitRows& a, const PreferenceTerms& t, float* logp, float* lse,
+                           hipStream_t s) {
     const unsigned g = grid_of(a.rows * a.parts);
-    if (a.vocab <= kWaveRow) {
-        if (a.f32)
-            hipLaunchKernelGGL((row_stats_kernel<float, 64, PREF>), dim3(g), dim3(64), 0, s, a, t);
-        else
-            hipLaunchKernelGGL((row_stats_kernel<uint16_t, 64, PREF>), dim3(g), dim3(64), 0, s, a, t);
-    } else {
-        if (a.f32)
-            hipLaunchKernelGGL((row_stats_kernel<float, 256, PREF>), dim3(g), dim3(256), 0, s, a, t);
-        else
-            hipLaunchKernelGGL((row_stats_kernel<uint16_t, 256, PREF>), dim3(g), dim3(256), 0, s, a, t);
-    }
+    if (a.f32)
+        hipLaunchKernelGGL((row_stats_kernel<float, NT, MODE>), dim3(g), dim3(NT), 0, s, a, t, logp, lse);
+    else
+        hipLaunchKernelGGL((row_stats_kernel<uint16_t, NT, MODE>), dim3(g), dim3(NT), 0, s, a, t, logp,
+                           lse);
     return hipGetLastError();
 }
 
-int64_t grad_spans(int64_t vocab) { return (vocab + kGradSpan - 1) / kGradSpan; }
+template <int MODE>
+hipError_t launch_stats(const LogitRows& a, const PreferenceTerms& t, float* logp, float* lse,
+                        hipStream_t s) {
+    return row_bytes(a) <= kWaveRow ? launch_stats_nt<64, MODE>(a, t, logp, lse, s)
+                                    : launch_stats_nt<256, MODE>(a, t, logp, lse, s);
+}
+
+// Values of a row that one workgroup of the split gradient kernels writes:
+// 4470 of 6697 rows x 128256 bf16 take 464 us in spans of 4096 (6.2 TB/s),
+// 611 us of 2048, 515 of 8192, 505 to 520 of more.
+constexpr int64_t kGradSpan = 4096;
+int grad_spans(int64_t vocab) { return (int)((vocab + kGradSpan - 1) / kGradSpan); }
+
+// Up to this many rows of the policy loss are split over workgroups, more
+// take one each (us, split against the best of one each): 16 x 129280
+// binary32 12 / 27, 64 x 23 / 28, 128 x 39 / 32; 64 x 128256 bf16 18 / 26,
+// 128 x 27 / 26; 64 x 8192 8.9 / 8.8.
+constexpr int64_t kSplitRows = 64;
+
+// Threads of a row's workgroup.  Long rows want many, as held pieces are
+// what is not read twice; many short rows want small workgroups, as a row's
+// start and end take a few us (us at 64 / 256 / 512 / 1024 threads, bf16):
+// 4000 x 1000 13 / 23 / 37 / 80, 4000 x 8192 31 / 37 / 52 / 91, 512 x 8192
+// 15 / 11 / 11 / 16, 4000 x 32000 119 / 97 / 100 / 150, 512 x 32000 37 / 21 /
+// 19 / 25, 4000 x 64000 254 / 202 / 186 / 238, 4000 x 128256 543 / 437 / 394 /
+// 441, 256 x 128256 113 / 42 / 34 / 32; binary32: 1500 x 129280 407 / 361 /
+// 326 / 300, 1500 x 60000 179 / 159 / 141 / 143.
+int policy_row_threads(int64_t rows, int64_t bytes) {
+    if (bytes > (256 << 10)) return 1024;
+    if (rows <= 256) return bytes > (128 << 10) ? 1024 : 512;
+    if (bytes > (64 << 10)) return 512;
+    if (rows <= 512) return bytes > (16 << 10) ? 512 : 256;
+    return rows >= 2048 && bytes <= (16 << 10) ? 64 : 256;
+}
+
+template <int NT>
+hipError_t launch_policy_rows(const LogitRows& a, const PolicyTerms& t, void* d, int64_t ldd,
+                              float* logp, hipStream_t s) {
+    constexpr int64_t kMost = int64_t(1) << 21;  // fewer than 2^32 threads a launch
+    for (int64_t row0 = 0; row0 < a.rows; row0 += kMost) {
+        const unsigned g = (unsigned)std::min(a.rows - row0, kMost);
+        if (a.f32)
+            hipLaunchKernelGGL((policy_row_kernel<float, NT>), dim3(g), dim3(NT), 0, s, a, t, row0,
+                               (float*)d, ldd, logp);
+        else
+            hipLaunchKernelGGL((policy_row_kernel<uint16_t, NT>), dim3(g), dim3(NT), 0, s, a, t, row0,
+                               (uint16_t*)d, ldd, logp);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
 
 }  // namespace
 
 int32_t stat_parts(int64_t rows, int64_t vocab) {
-    if (rows < 1) return 1;
-    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(32, vocab / 4096));
-    return (int32_t)std::min(most, std::max<int64_t>(1, 1024 / rows));
+    int32_t parts = 1;
+    while (rows > 0 && parts < 32 && rows * 2 * parts <= 1024 && vocab >= 2 * parts * 4096) parts *= 2;
+    return parts;
 }
 
 hipError_t launch_token_logp(const LogitRows& a, float* logp, float* lse, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
-    hipError_t e = launch_stats<false>(a, PreferenceTerms{}, s);
+    if (a.parts == 1) return launch_stats<STATS_LOGP>(a, PreferenceTerms{}, logp, lse, s);
+    hipError_t e = launch_stats<STATS_ONLY>(a, PreferenceTerms{}, nullptr, nullptr, s);
     if (e != hipSuccess) return e;
-    const int64_t wgs = (a.rows + 255) / 256;
-    hipLaunchKernelGGL(logp_kernel, dim3(grid_of(wgs)), dim3(256), 0, s, a, logp, lse);
+    hipLaunchKernelGGL(logp_kernel, dim3((unsigned)((a.rows * a.parts + 255) / 256)), dim3(256), 0, s, a,
+                       logp, lse);
     return hipGetLastError();
 }
 
 hipError_t launch_policy(const LogitRows& a, const PolicyTerms& t, void* d, int64_t ldd,
                          float* logp, float* stats, hipStream_t s) {
-    if (a.rows > 0) {
-        hipError_t e = launch_stats<false>(a, PreferenceTerms{}, s);
-        if (e != hipSuccess) return e;
+    if (a.rows <= kSplitRows) {
+        hipError_t e;
+        if (a.rows > 0) {
+            e = launch_stats<STATS_ONLY>(a, PreferenceTerms{}, nullptr, nullptr, s);
+            if (e != hipSuccess) return e;
+        }
+        const int spans = grad_spans(a.vocab);
+        const unsigned g = 1 + (d ? (unsigned)(a.rows * spans) : 0);
+        if (a.f32)
+            hipLaunchKernelGGL((policy_grad_kernel<float, 256>), dim3(g), dim3(256), 0, s, a, t,
+                               (float*)d, ldd, spans, logp, stats);
+        else
+            hipLaunchKernelGGL((policy_grad_kernel<uint16_t, 256>), dim3(g), dim3(256), 0, s, a, t,
+                               (uint16_t*)d, ldd, spans, logp, stats);
+        return hipGetLastError();
     }
-    const int64_t spans = grad_spans(a.vocab);
-    const unsigned g = 1 + (d ? grid_of(a.rows * spans) : 0);
-    if (a.f32)
-        hipLaunchKernelGGL((policy_grad_kernel<float, 256>), dim3(g), dim3(256), 0, s, a, t,
-                           (float*)d, ldd, spans, logp, stats);
-    else
-        hipLaunchKernelGGL((policy_grad_kernel<uint16_t, 256>), dim3(g), dim3(256), 0, s, a, t,
-                           (uint16_t*)d, ldd, spans, logp, stats);
+    const int nt = policy_row_threads(a.rows, row_bytes(a));
+    hipError_t e = nt == 64    ? launch_policy_rows<64>(a, t, d, ldd, logp, s)
+                   : nt == 256 ? launch_policy_rows<256>(a, t, d, ldd, logp, s)
+                   : nt == 512 ? launch_policy_rows<512>(a, t, d, ldd, logp, s)
+                               : launch_policy_rows<1024>(a, t, d, ldd, logp, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(policy_sum_kernel, dim3(1), dim3(1024), 0, s, t, a.rows, stats);
     return hipGetLastError();
 }
 
-hipError_t launch_preference(const LogitRows& a, const PreferenceTerms& t, void* d, int64_t ldd,
+hipError_t launch_preference(const LogitRows& a, const PreferenceTerms& t0, void* d, int64_t ldd,
                              float* seq_logp, float* stats, hipStream_t s) {
     hipError_t e;
+    // The statistics keep the last rows in the 256 MB memory-side cache for
+    // the gradient (2003 x 50000 binary32, 400 MB: 52 + 147 us all past the
+    // cache, 54 + 120 so; with everything through it the statistics of 1.7
+    // GB take 203 us instead of 178).
+    constexpr int64_t kCache = int64_t(256) << 20;
+    PreferenceTerms t = t0;
+    t.kept_from = d ? std::max<int64_t>(0, a.rows - kCache / row_bytes(a)) : a.rows;
     if (a.rows > 0) {
-        e = launch_stats<true>(a, t, s);
+        e = launch_stats<STATS_MARK>(a, t, nullptr, nullptr, s);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((pair_kernel<256>), dim3((unsigned)t.pairs), dim3(256), 0, s, a, t, seq_logp);
+    hipLaunchKernelGGL((pair_kernel<1024>), dim3((unsigned)t.pairs), dim3(1024), 0, s, a, t, seq_logp);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t spans = grad_spans(a.vocab);
+    const int spans = grad_spans(a.vocab);
     const unsigned g = 1 + (d ? grid_of(a.rows * spans) : 0);
     if (a.f32)
         hipLaunchKernelGGL((preference_grad_kernel<float, 256>), dim3(g), dim3(256), 0, s, a, t,

@@ -15,12 +15,12 @@ namespace {
 
 using namespace rs::rowcheck;
 
-constexpr int64_t kMaxPairs = int64_t(1) << 23;  // one workgroup each in one launch
+constexpr int64_t kMaxPairs = int64_t(1) << 21;  // one workgroup each in one launch
 
-// Scratch: row statistics, token logits; for the preference loss also marks,
-// coefficients and the pairs' sums.
+// Scratch: row statistics, token logits, the sums of rows or pairs; for the
+// preference loss also marks and what the rows' gradients take.
 struct Scratch {
-    size_t stat = 0, token = 0, mark = 0, coef = 0, terms = 0, bytes = 0;
+    size_t stat = 0, token = 0, mark = 0, grad = 0, terms = 0, bytes = 0;
 };
 
 Scratch scratch_of(int64_t rows, int64_t vocab, int64_t n_seq) {
@@ -33,10 +33,10 @@ Scratch scratch_of(int64_t rows, int64_t vocab, int64_t n_seq) {
     };
     s.stat = take(size_t(rows) * rs::stat_parts(rows, vocab) * sizeof(rs::RowStat));
     s.token = take(size_t(rows) * sizeof(float));
+    s.terms = take(size_t(std::max(rows, n_seq / 2)) * 3 * sizeof(double));
     if (n_seq > 0) {
         s.mark = take(size_t(rows) * sizeof(int32_t));
-        s.coef = take(size_t(rows) * sizeof(float));
-        s.terms = take(size_t(n_seq / 2) * 3 * sizeof(double));
+        s.grad = take(size_t(rows) * sizeof(rs::GradRow));
     }
     s.bytes = std::max<size_t>(at, 256);
     return s;
@@ -140,6 +140,7 @@ rs_status rs_policy_loss(const void* d_logits, int32_t dtype, int64_t rows, int6
     t.lo = 1.0 - hp->clip_low;
     t.hi = 1.0 + hp->clip_high;
     t.kl_coef = hp->kl_coef;
+    t.terms = reinterpret_cast<double*>(static_cast<uint8_t*>(d_work) + sc.terms);
     hipError_t e = rs::launch_policy(a, t, d_dlogits, ldd, d_logp, d_stats, as_stream(stream));
     if (e != hipSuccess) return hip_fail(e, "policy_loss launch");
     return RS_OK;
@@ -152,7 +153,7 @@ rs_status rs_preference_loss(const void* d_logits, int32_t dtype, int64_t rows, 
                              float* d_seq_logp, float* d_stats, void* d_work, size_t bytes,
                              void* stream) {
     if (!hp || !d_stats || !d_start) return fail(RS_EINVAL, "NULL argument");
-    if (n_pairs < 1 || n_pairs > kMaxPairs) return fail(RS_EINVAL, "number of pairs outside 1..2^23");
+    if (n_pairs < 1 || n_pairs > kMaxPairs) return fail(RS_EINVAL, "number of pairs outside 1..2^21");
     rs::LogitRows a;
     Scratch sc;
     rs_status st = fill_rows(d_logits, dtype, rows, vocab, ld, d_target, hp->temperature, d_work,
@@ -183,7 +184,7 @@ rs_status rs_preference_loss(const void* d_logits, int32_t dtype, int64_t rows, 
     t.kind = hp->kind;
     t.average = hp->average;
     t.mark = reinterpret_cast<int32_t*>(w + sc.mark);
-    t.coef = reinterpret_cast<float*>(w + sc.coef);
+    t.grad = reinterpret_cast<rs::GradRow*>(w + sc.grad);
     t.terms = reinterpret_cast<double*>(w + sc.terms);
     hipError_t e = rs::launch_preference(a, t, d_dlogits, ldd, d_seq_logp, d_stats, as_stream(stream));
     if (e != hipSuccess) return hip_fail(e, "preference_loss launch");

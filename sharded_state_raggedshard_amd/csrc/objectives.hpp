@@ -16,6 +16,12 @@ struct ExpScale {
     float hi, lo;
 };
 
+// What the gradient kernels take of a row (grad_row() fills it).
+struct GradRow {
+    float m, f, own;
+    int32_t y;
+};
+
 // Maximum and sum of exponentials of (a part of) a row.
 struct RowStat {
     double s;
@@ -42,6 +48,7 @@ struct PolicyTerms {
     const float* ref_logp;  // nullable: no KL term
     const float* advantage;
     double lo, hi, kl_coef;  // the ratio's bounds
+    double* terms;           // scratch: three sums per row
 };
 
 struct PreferenceTerms {
@@ -51,9 +58,10 @@ struct PreferenceTerms {
     const float* weight;    // nullable
     double beta, smoothing, margin;
     int32_t kind, average;
-    // scratch: a mark and a coefficient per row, three sums per pair
+    int64_t kept_from;  // rows from here on stay cached (launch_preference() sets it)
+    // scratch: a mark and a GradRow per row, three sums per pair
     int32_t* mark;
-    float* coef;
+    GradRow* grad;
     double* terms;
 };
 
