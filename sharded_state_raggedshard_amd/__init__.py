@@ -173,10 +173,26 @@ def _ptr(x) -> Optional[int]:
     return int(x.data_ptr())
 
 
+_current_stream = None
+
+
+def _stream_reader():
+    """Reads the handle of torch's current stream.  torch's raw-handle reader
+    takes 0.3 us where building a Stream object takes 3."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return lambda: int(torch.cuda.current_stream().cuda_stream)
+    device = torch.cuda.current_device
+    return lambda: raw(device())
+
+
 def _stream(stream) -> Optional[int]:
+    global _current_stream
     if stream is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        if _current_stream is None:
+            _current_stream = _stream_reader()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)

@@ -37,7 +37,7 @@ struct RouterBalance {
 struct RouterChunks {
     int64_t n, rows;
 };
-RouterChunks router_chunks(int64_t rows, int32_t experts);
+RouterChunks router_chunks(int64_t rows);
 
 hipError_t launch_router_balance(const RouterBalance& a, hipStream_t s);
 
