@@ -210,8 +210,9 @@ enum { MARK_OUTSIDE = 0, MARK_ZERO = 1, MARK_TOKEN = 2 };
 
 // What row_stats_kernel does beside the statistics: nothing; writes logp (and
 // lse) of whole rows; marks rows for the preference loss (outside every
-// sequence, without a token, with one).
-enum { STATS_ONLY = 0, STATS_LOGP = 1, STATS_MARK = 2 };
+// sequence, without a token, with one); nothing, but leaves the logits in the
+// caches for the gradient.
+enum { STATS_ONLY = 0, STATS_LOGP = 1, STATS_MARK = 2, STATS_KEEP = 3 };
 
 __device__ __forceinline__ void write_logp(const LogitRows& a, int64_t row, const RowEnd& e,
                                            float token, float* logp, float* lse) {
@@ -252,7 +253,7 @@ __global__ __launch_bounds__(NT) void row_stats_kernel(LogitRows a, PreferenceTe
         const float token = Vec<T>::one(z[a.target[row]]);
         const Pieces<T> ps(z, a.vocab);
         MaxSum run;
-        if (MODE == STATS_MARK && row >= t.kept_from)
+        if (MODE == STATS_KEEP || (MODE == STATS_MARK && row >= t.kept_from))
             take_part<T, NT, false>(run, z, ps, part_of(z, ps, part, a.parts), k);
         else
             take_part<T, NT, true>(run, z, ps, part_of(z, ps, part, a.parts), k);
@@ -367,22 +368,30 @@ __device__ __forceinline__ u32x4 grad16(const GradRow& g, const u32x4& w, ExpSca
     return Vec<T>::close(x);
 }
 
-// The gradient of a part of a row.
-template <typename T, int NT>
+// The gradient of a part of a row; get() gives the row's GradRow to every
+// thread, after the first loads are under way.
+template <typename T, int NT, typename F>
 __device__ __forceinline__ void grad_part(const T* z, T* d, const Pieces<T>& ps, Part part,
-                                          ExpScale k, const GradRow& g) {
+                                          ExpScale k, F get) {
     constexpr int N = Vec<T>::n, U = 4;
     const int tid = threadIdx.x;
     const T* from = z + ps.head;
     T* to = d + ps.head;
-    for (int v = part.v0 + tid; v < part.v1; v += U * NT) {
-        u32x4 w[U];
+    u32x4 w[U];
+    const auto load = [&](int v) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (v + u * NT < part.v1) w[u] = load16_once(from + (v + u * NT) * N);
+    };
+    int v = part.v0 + tid;
+    load(v);
+    const GradRow g = get();
+    while (v < part.v1) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (v + u * NT < part.v1) store16(to + (v + u * NT) * N, grad16<T>(g, w[u], k));
+        v += U * NT;
+        load(v);
     }
     if (part.ends && tid < ps.edges)
         d[ps.edge(tid)] = Vec<T>::pack(grad_one(g, Vec<T>::one(z[ps.edge(tid)]), k));
@@ -403,6 +412,12 @@ __device__ __forceinline__ void zero_part(T* d, const Pieces<T>& ps, Part part) 
 
 // ------------------------------------------------------- policy loss, split
 
+// Up to this many rows of the policy loss are split over workgroups, more
+// take one each (us, split against the best of one each): 16 x 129280
+// binary32 12 / 27, 64 x 23 / 28, 128 x 39 / 32; 64 x 128256 bf16 18 / 26,
+// 128 x 27 / 26; 64 x 8192 8.9 / 8.8.
+constexpr int64_t kSplitRows = 64;
+
 // Few long rows: row_stats_kernel over parts, then this kernel, in which
 // workgroup 0 computes the rows' outputs and the loss sums and every other
 // one writes a part of a row's gradient.
@@ -415,20 +430,26 @@ __global__ __launch_bounds__(NT) void policy_grad_kernel(LogitRows a, PolicyTerm
     const int tid = threadIdx.x;
     const ExpScale k = a.k;
     if (blockIdx.x == 0) {
-        double pg = 0.0, kl = 0.0, cl = 0.0;
-        const int part = tid % a.parts;
-        for (int64_t row = tid / a.parts; row < a.rows; row += NT / a.parts) {
-            PolicyRow p;
-            if (has_token(a, row)) {
-                const float token = a.token[row];
-                const RowEnd e = row_end(join_parts(a, row, part));
-                if (part == 0) p = policy_row(a, t, row, e, token);
+        // four lanes a row (all rows at once: this workgroup is the one that
+        // the launch waits for)
+        static_assert(NT == 4 * kSplitRows, "four lanes a row");
+        const int64_t row = tid / 4;
+        const int sub = tid % 4, per = a.parts < 4 ? 1 : a.parts / 4;
+        PolicyRow p;
+        if (row < a.rows) {
+            const float token = a.token[row];
+            MaxSum x;
+            if (sub * per < a.parts) {
+                const RowStat* q = a.stat + row * a.parts + sub * per;
+                x = MaxSum{q[0].m, q[0].s};
+                for (int i = 1; i < per; ++i) x.join(q[i].m, q[i].s, k);
             }
-            pg += p.pg;
-            kl += p.kl;
-            cl += p.clipped;
-            if (part == 0 && logp) logp[row] = (float)p.logp;
+            x.join(__shfl_xor(x.m, 1, 64), __shfl_xor(x.s, 1, 64), k);
+            x.join(__shfl_xor(x.m, 2, 64), __shfl_xor(x.s, 2, 64), k);
+            if (sub == 0 && has_token(a, row)) p = policy_row(a, t, row, row_end(x), token);
+            if (sub == 0 && logp) logp[row] = (float)p.logp;
         }
+        const double pg = p.pg, kl = p.kl, cl = p.clipped;
         const double sum[3] = {wg_sum<NT>(pg, lds), wg_sum<NT>(kl, lds), wg_sum<NT>(cl, lds)};
         if (tid == 0) policy_stats(t, sum, stats);
         return;
@@ -439,20 +460,23 @@ __global__ __launch_bounds__(NT) void policy_grad_kernel(LogitRows a, PolicyTerm
     T* to = d + row * ldd;
     const Pieces<T> ps(z, a.vocab);
     const Part part = part_of(z, ps, span, spans);
-    bool live = has_token(a, row);
-    if (live) {
-        const RowEnd e = row_end(join_parts(a, row, tid % a.parts));
-        live = !e.empty;
-        if (live && tid == 0) {
-            const float token = a.token[row];
-            g = grad_row(e, policy_row(a, t, row, e, token).coef * a.scale, a.target[row], token, k);
-        }
-    }
-    __syncthreads();
-    if (live)
-        grad_part<T, NT>(z, to, ps, part, k, g);
-    else
+    if (!has_token(a, row)) {
         zero_part<T, NT>(to, ps, part);
+        return;
+    }
+    grad_part<T, NT>(z, to, ps, part, k, [&] {
+        const RowEnd e = row_end(join_parts(a, row, tid % a.parts));
+        if (tid == 0) {
+            g = GradRow{0.0f, 0.0f, 0.0f, -1};  // a row of nothing but -inf: zeros, no token
+            if (!e.empty) {
+                const float token = a.token[row];
+                g = grad_row(e, policy_row(a, t, row, e, token).coef * a.scale, a.target[row],
+                             token, k);
+            }
+        }
+        __syncthreads();
+        return g;
+    });
 }
 
 // ------------------------------------------------------ policy loss, by row
@@ -527,7 +551,7 @@ __global__ __launch_bounds__(NT, 4) void policy_row_kernel(LogitRows a, PolicyTe
         if (j * NT + tid < ps.n) store16(to + ps.head + (j * NT + tid) * N, grad16<T>(gr, w[j], k));
     const int yv = ps.piece(gr.y);
     if (yv >= 0 && yv < kHeld * NT && yv % NT == tid) to[gr.y] = Vec<T>::pack(gr.own);
-    grad_part<T, NT>(z, to, ps, Part{kHeld * NT, ps.n, true}, k, gr);
+    grad_part<T, NT>(z, to, ps, Part{kHeld * NT, ps.n, true}, k, [&] { return gr; });
 }
 
 __global__ __launch_bounds__(1024) void policy_sum_kernel(PolicyTerms t, int64_t rows, float* stats) {
@@ -539,40 +563,57 @@ __global__ __launch_bounds__(1024) void policy_sum_kernel(PolicyTerms t, int64_t
 
 // ---------------------------------------------------------- preference loss
 
-// One workgroup per pair: its sequences' log-probabilities, its loss and
-// what its rows' gradients take.
+// One workgroup per pair, half of it per sequence: the sequences'
+// log-probabilities, the loss and what the rows' gradients take.
 template <int NT>
 __global__ __launch_bounds__(NT) void pair_kernel(LogitRows a, PreferenceTerms t, float* seq_logp) {
-    __shared__ double lds[NT / 64];
-    __shared__ double sum[2], count[2], slope;
+    constexpr int HALF = NT / 2, WAVES = HALF / 64;
+    __shared__ double logp_lds[2 * WAVES], tokens_lds[2 * WAVES];
+    __shared__ double factor[2];  // dloss / dlogp / T of a side's rows
     const ExpScale k = a.k;
-    const int tid = threadIdx.x;
-    const int64_t p = blockIdx.x;
+    const int tid = threadIdx.x, side = tid / HALF, at = tid % HALF;
+    const int64_t p = blockIdx.x, q = p + side * t.pairs;
     const double w = t.weight ? (double)t.weight[p] : 1.0 / (double)t.pairs;
-    for (int side = 0; side < 2; ++side) {
-        const int64_t q = p + side * t.pairs;
-        const int64_t r0 = min(max(t.start[q], int64_t(0)), a.rows);
-        const int64_t r1 = min(max(t.start[q + 1], r0), a.rows);
-        double l = 0.0, n = 0.0;
-        for (int64_t row = r0 + tid; row < r1; row += NT) {
-            if (t.mark[row] != MARK_TOKEN) continue;
-            const RowEnd e = row_of(a, row, k);
-            if (e.empty) {
-                t.mark[row] = MARK_ZERO;
-                continue;
-            }
-            l += logp_of(e, a.token[row], a.scale);
-            n += 1.0;
+    int64_t r0 = t.start[q], r1 = t.start[q + 1];
+    if (r0 < 0) r0 = 0;
+    if (r1 > a.rows) r1 = a.rows;
+    double l = 0.0, n = 0.0;
+    RowEnd first;  // of the thread's first row
+    first.empty = true;
+    for (int64_t row = r0 + at; row < r1; row += HALF) {
+        if (t.mark[row] != MARK_TOKEN) continue;
+        const RowEnd e = row_of(a, row, k);
+        if (row == r0 + at) first = e;
+        if (e.empty) {
+            t.mark[row] = MARK_ZERO;
+            continue;
         }
-        l = wg_sum<NT>(l, lds);
-        n = wg_sum<NT>(n, lds);
-        if (tid == 0) {
-            count[side] = t.average ? fmax(n, 1.0) : 1.0;
-            sum[side] = l / count[side];
-            if (seq_logp) seq_logp[q] = (float)sum[side];
-        }
+        l += logp_of(e, a.token[row], a.scale);
+        n += 1.0;
     }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+        l += __shfl_xor(l, off, 64);
+        n += __shfl_xor(n, off, 64);
+    }
+    if ((tid & 63) == 0) {
+        logp_lds[tid >> 6] = l;
+        tokens_lds[tid >> 6] = n;
+    }
+    __syncthreads();
     if (tid == 0) {
+        double sum[2], count[2];
+        for (int i = 0; i < 2; ++i) {
+            sum[i] = 0.0;
+            count[i] = 0.0;
+            for (int v = 0; v < WAVES; ++v) {
+                sum[i] += logp_lds[i * WAVES + v];
+                count[i] += tokens_lds[i * WAVES + v];
+            }
+            count[i] = t.average ? fmax(count[i], 1.0) : 1.0;
+            sum[i] /= count[i];
+            if (seq_logp) seq_logp[p + i * t.pairs] = (float)sum[i];
+        }
         double D = sum[0] - sum[1];
         if (t.ref_logp && w != 0.0) D -= (double)t.ref_logp[p] - (double)t.ref_logp[p + t.pairs];
         const double h = t.beta * D - t.margin;
@@ -596,17 +637,16 @@ __global__ __launch_bounds__(NT) void pair_kernel(LogitRows a, PreferenceTerms t
         t.terms[3 * p] = out ? 0.0 : w * loss;
         t.terms[3 * p + 1] = out ? 0.0 : w * h;
         t.terms[3 * p + 2] = out || !(h > 0.0) ? 0.0 : w;
-        slope = out ? 0.0 : w * g * a.scale;
+        const double slope = out ? 0.0 : w * g * a.scale;
+        factor[0] = slope / count[0];
+        factor[1] = -slope / count[1];
     }
     __syncthreads();
-    for (int side = 0; side < 2; ++side) {
-        const int64_t q = p + side * t.pairs;
-        const int64_t r0 = min(max(t.start[q], int64_t(0)), a.rows);
-        const int64_t r1 = min(max(t.start[q + 1], r0), a.rows);
-        const double cs = (side ? -slope : slope) / count[side];
-        for (int64_t row = r0 + tid; row < r1; row += NT)
-            if (t.mark[row] == MARK_TOKEN)
-                t.grad[row] = grad_row(row_of(a, row, k), cs, a.target[row], a.token[row], k);
+    const double cs = factor[side];
+    for (int64_t row = r0 + at; row < r1; row += HALF) {
+        if (t.mark[row] != MARK_TOKEN) continue;
+        const RowEnd e = row == r0 + at ? first : row_of(a, row, k);
+        t.grad[row] = grad_row(e, cs, a.target[row], a.token[row], k);
     }
 }
 
@@ -640,7 +680,7 @@ __global__ __launch_bounds__(NT) void preference_grad_kernel(LogitRows a, Prefer
         if (mark == MARK_ZERO)
             zero_part<T, NT>(to, ps, part);
         else
-            grad_part<T, NT>(z, to, ps, part, a.k, t.grad[row]);
+            grad_part<T, NT>(z, to, ps, part, a.k, [&] { return t.grad[row]; });
     }
 }
 
@@ -668,17 +708,11 @@ hipError_t launch_stats(const LogitRows& a, const PreferenceTerms& t, float* log
                                     : launch_stats_nt<256, MODE>(a, t, logp, lse, s);
 }
 
-// Values of a row that one workgroup of the split gradient kernels writes:
-// 4470 of 6697 rows x 128256 bf16 take 464 us in spans of 4096 (6.2 TB/s),
-// 611 us of 2048, 515 of 8192, 505 to 520 of more.
+// Values of a row that one workgroup of the preference gradient writes: 4470
+// of 6697 rows x 128256 bf16 take 464 us in spans of 4096 (6.2 TB/s), 611 of
+// 2048, 515 of 8192, 505 to 520 of more.
 constexpr int64_t kGradSpan = 4096;
 int grad_spans(int64_t vocab) { return (int)((vocab + kGradSpan - 1) / kGradSpan); }
-
-// Up to this many rows of the policy loss are split over workgroups, more
-// take one each (us, split against the best of one each): 16 x 129280
-// binary32 12 / 27, 64 x 23 / 28, 128 x 39 / 32; 64 x 128256 bf16 18 / 26,
-// 128 x 27 / 26; 64 x 8192 8.9 / 8.8.
-constexpr int64_t kSplitRows = 64;
 
 // Threads of a row's workgroup.  Long rows want many, as held pieces are
 // what is not read twice; many short rows want small workgroups, as a row's
@@ -737,10 +771,13 @@ hipError_t launch_policy(const LogitRows& a, const PolicyTerms& t, void* d, int6
     if (a.rows <= kSplitRows) {
         hipError_t e;
         if (a.rows > 0) {
-            e = launch_stats<STATS_ONLY>(a, PreferenceTerms{}, nullptr, nullptr, s);
+            e = launch_stats<STATS_KEEP>(a, PreferenceTerms{}, nullptr, nullptr, s);
             if (e != hipSuccess) return e;
         }
-        const int spans = grad_spans(a.vocab);
+        // 16 KB a workgroup, one round of loads: more cost more starts than
+        // they win (61 x 201088 bf16 19 us, of 8 KB 21; 16 x 129280 binary32
+        // 11 us, of 32 KB 12)
+        const int spans = (int)((row_bytes(a) + (16 << 10) - 1) / (16 << 10));
         const unsigned g = 1 + (d ? (unsigned)(a.rows * spans) : 0);
         if (a.f32)
             hipLaunchKernelGGL((policy_grad_kernel<float, 256>), dim3(g), dim3(256), 0, s, a, t,

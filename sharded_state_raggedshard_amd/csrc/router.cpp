@@ -21,7 +21,7 @@ struct Scratch {
 };
 
 Scratch scratch_of(int64_t rows, int32_t experts, int64_t n_seq) {
-    const rs::RouterChunks c = rs::router_chunks(rows);
+    const rs::RouterChunks c = rs::router_chunks(rows, n_seq);
     Scratch s;
     s.part = align256(size_t(n_seq) * sizeof(int32_t));
     s.loss = s.part + align256(size_t(c.n + n_seq) * size_t(experts) * sizeof(float));

@@ -37,7 +37,7 @@ struct RouterBalance {
 struct RouterChunks {
     int64_t n, rows;
 };
-RouterChunks router_chunks(int64_t rows);
+RouterChunks router_chunks(int64_t rows, int64_t n_seq);
 
 hipError_t launch_router_balance(const RouterBalance& a, hipStream_t s);
 

@@ -96,6 +96,29 @@ __global__ __launch_bounds__(kCountThreads) void router_count_kernel(RouterBalan
     }
 }
 
+// The same for short sequences, straight to the outputs: a thread a row.
+// Needs a.start.
+__global__ __launch_bounds__(kThreads) void router_count_short_kernel(RouterBalance a) {
+    const int64_t row = blockIdx.x * (int64_t)kThreads + threadIdx.x;
+    if (row >= a.rows || (a.mask && !a.mask[row])) return;
+    int64_t s = 0;  // number of entries start[1 .. n_seq] that are <= row
+    for (int64_t n = a.n_seq; n > 0;) {
+        const int64_t half = (n + 1) / 2;
+        if (a.start[s + half] <= row) {
+            s += half;
+            n -= half;
+        } else {
+            n = half - 1;
+        }
+    }
+    if (s >= a.n_seq || a.start[0] > row) return;
+    atomicAdd(&a.tokens[s], 1);
+    for (int j = 0; j < a.k; ++j) {
+        const int64_t e = a.topk[row * a.ldk + j];
+        if (e >= 0 && e < a.experts) atomicAdd(&a.counts[s * a.experts + e], 1);
+    }
+}
+
 // Sum over groups of L neighbouring lanes, in every lane: cross-lane moves
 // inside the vector unit (a shuffle through LDS takes about 100 cycles).
 template <int CTRL>
@@ -380,6 +403,9 @@ __global__ __launch_bounds__(kThreads, NV == 1 ? 4 : 1) void router_main_kernel(
     }
 }
 
+// Average rows of a sequence below which rows are counted without LDS.
+constexpr int64_t kShort = 256;
+
 // Everything by one workgroup, for batches where the launches would take
 // longer than the work.
 template <typename T, int L, int NV, bool SIGMOID, bool FULL>
@@ -422,22 +448,23 @@ __global__ __launch_bounds__(kThreads) void router_small_kernel(RouterBalance a)
 
 // Workgroup (s, b): mean probabilities of `columns` (a power of two) columns
 // of a sequence; the last workgroup: the losses.
-__global__ __launch_bounds__(1024) void router_finish_kernel(RouterBalance a, int64_t chunks,
+template <int NT>
+__global__ __launch_bounds__(NT) void router_finish_kernel(RouterBalance a, int64_t chunks,
                                                              int64_t per, int64_t blocks,
                                                              int columns) {
-    __shared__ double lds[1024];
+    __shared__ double lds[NT];
     const int tid = threadIdx.x;
     if (blockIdx.x == a.n_seq * blocks) {
         for (int i = 0; i < 2; ++i) {
             double v = 0.0;
-            for (int64_t c = tid; c < chunks; c += 1024) v += a.loss[2 * c + i];
-            v = wg_sum<1024>(v, lds);
+            for (int64_t c = tid; c < chunks; c += NT) v += a.loss[2 * c + i];
+            v = wg_sum<NT>(v, lds);
             if (tid == 0) a.stats[i] = (float)v;
         }
         return;
     }
     const int64_t s = blockIdx.x / blocks;
-    const int lanes = 1024 / columns;
+    const int lanes = NT / columns;
     const int e = (int)(blockIdx.x - s * blocks) * columns + tid % columns;
     int64_t lo, hi;
     clip_rows(a, s, 0, a.rows, lo, hi);
@@ -515,15 +542,20 @@ hipError_t launch_main(const RouterBalance& a, const RouterChunks& c, hipStream_
 
 }  // namespace
 
-RouterChunks router_chunks(int64_t rows) {
+RouterChunks router_chunks(int64_t rows, int64_t n_seq) {
+    // one round of the 1024 workgroups the device holds, not below 32 rows
+    // each (with 16, the last kernel's sums take longer than is won), but no
+    // more than a sequence: a workgroup takes its sequences one after another
+    // (40 rows in 60 sequences: 114 us in two chunks)
     RouterChunks c;
-    c.rows = std::max<int64_t>(32, (rows + 1023) / 1024);
+    const int64_t least = std::min<int64_t>(32, std::max<int64_t>(1, rows / n_seq));
+    c.rows = std::max<int64_t>(least, (rows + 1023) / 1024);
     c.n = (rows + c.rows - 1) / c.rows;
     return c;
 }
 
 hipError_t launch_router_balance(const RouterBalance& a, hipStream_t s) {
-    const RouterChunks c = router_chunks(a.rows);
+    const RouterChunks c = router_chunks(a.rows, a.n_seq);
     if (small_batch(a)) return launch_main(a, c, s);
     const int64_t cells = a.n_seq * a.experts;
     const int64_t zero = (std::max<int64_t>(cells, a.n_seq) + kThreads - 1) / kThreads;
@@ -532,9 +564,15 @@ hipError_t launch_router_balance(const RouterBalance& a, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (c.n > 0) {
-        const int64_t per = std::max<int64_t>(kCountThreads, (a.rows + 255) / 256);
-        hipLaunchKernelGGL(router_count_kernel, dim3((unsigned)((a.rows + per - 1) / per)),
-                           dim3(kCountThreads), 0, s, a, per);
+        if (a.start && a.rows / a.n_seq < kShort) {
+            hipLaunchKernelGGL(router_count_short_kernel,
+                               dim3((unsigned)((a.rows + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+                               s, a);
+        } else {
+            const int64_t per = std::max<int64_t>(kCountThreads, (a.rows + 255) / 256);
+            hipLaunchKernelGGL(router_count_kernel, dim3((unsigned)((a.rows + per - 1) / per)),
+                               dim3(kCountThreads), 0, s, a, per);
+        }
         e = hipGetLastError();
         if (e != hipSuccess) return e;
         e = launch_main(a, c, s);
@@ -544,8 +582,13 @@ hipError_t launch_router_balance(const RouterBalance& a, hipStream_t s) {
     // sequence: 7.1 -> 5.6 us; 61 sequences of 256 experts: 4.6 -> 6.2)
     const int columns = a.n_seq < 8 ? 16 : 32;
     const int64_t blocks = (a.experts + columns - 1) / columns;
-    hipLaunchKernelGGL(router_finish_kernel, dim3((unsigned)(a.n_seq * blocks + 1)), dim3(1024), 0, s,
-                       a, c.n, c.rows, blocks, columns);
+    const dim3 g((unsigned)(a.n_seq * blocks + 1));
+    if (c.n >= 16 * a.n_seq)
+        hipLaunchKernelGGL(router_finish_kernel<1024>, g, dim3(1024), 0, s, a, c.n, c.rows, blocks,
+                           columns);
+    else
+        hipLaunchKernelGGL(router_finish_kernel<256>, g, dim3(256), 0, s, a, c.n, c.rows, blocks,
+                           columns);
     return hipGetLastError();
 }
 

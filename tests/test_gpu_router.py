@@ -90,6 +90,11 @@ CASES = [
     (None, 40, 1000, 1, 0, 0, rs.RS_F32, 0), (None, 33, 1024, 16, 0, 0, rs.RS_BF16, 0),
     (None, 20, 1023, 4, 0, 5, rs.RS_F32, 0), ([i * 3 for i in range(200)] + [700], 700, 16, 2, 0, 0, rs.RS_BF16, 0.1),
     (None, 150001, 8, 2, 0, 0, rs.RS_BF16, 0),
+    # shorter on average than a counting workgroup's share; as many sequences as rows; more; few long ones
+    ([min(5 + i * i // 3, 1300) for i in range(64)], 1302, 40, 4, 0, 0, rs.RS_F32, 0.1),
+    (list(range(91)), 90, 48, 2, 0, 0, rs.RS_BF16, 0),
+    ([i // 3 for i in range(121)], 40, 24, 2, 0, 0, rs.RS_F32, 0.2),
+    ([0, 900, 901, 4000, 4000, 9000, 9000, 9000, 9000, 9001, 9700], 9700, 24, 2, 0, 0, rs.RS_BF16, 0.1),
 ]
 
 
