@@ -316,7 +316,7 @@ __device__ __forceinline__ PolicyRow policy_row(const LogitRows& a, const Policy
     if (t.ref_logp) {
         const double away = (double)t.ref_logp[row] - p.logp, q = exp(away);
         p.kl = w * (q - away - 1.0);
-        slope += t.kl_coef * (1.0 - q);
+        if (t.kl_coef != 0.0) slope += t.kl_coef * (1.0 - q);
     }
     p.coef = w * slope;
     return p;
@@ -334,7 +334,7 @@ __device__ __forceinline__ void sum_terms(const double* terms, int64_t n, double
 
 __device__ __forceinline__ void policy_stats(const PolicyTerms& t, const double (&sum)[3],
                                              float* stats) {
-    stats[0] = (float)(sum[0] + (t.ref_logp ? t.kl_coef * sum[1] : 0.0));
+    stats[0] = (float)(sum[0] + (t.kl_coef != 0.0 ? t.kl_coef * sum[1] : 0.0));
     for (int j = 0; j < 3; ++j) stats[1 + j] = (float)sum[j];
 }
 

@@ -101,6 +101,18 @@ SHAPES = [
 IDS = [f"{r}x{v}+{p}@{s}-{'f32' if d == rs.RS_F32 else 'bf16'}-T{t}" for r, v, p, s, d, t in SHAPES]
 
 
+# more rows than are split over workgroups: every workgroup size, with all of a
+# row in registers and with a rest
+ROW_SHAPES = [
+    (65, 2047, 0, 1, rs.RS_F32, 1.0), (66, 40001, 0, 0, rs.RS_BF16, 1.0), (65, 70001, 3, 0, rs.RS_BF16, 1.0),
+    (65, 110003, 0, 1, rs.RS_BF16, 1.0), (67, 60001, 0, 0, rs.RS_F32, 0.8), (65, 70016, 0, 0, rs.RS_F32, 1.0),
+    (300, 40003, 0, 0, rs.RS_BF16, 1.0), (300, 60007, 1, 3, rs.RS_BF16, 1.0), (300, 3001, 0, 0, rs.RS_F32, 1.0),
+    (520, 9001, 0, 0, rs.RS_BF16, 1.3), (520, 30011, 0, 0, rs.RS_BF16, 1.0), (2100, 5003, 0, 0, rs.RS_BF16, 1.0),
+    (2100, 8111, 2, 1, rs.RS_BF16, 1.0), (2100, 7, 0, 0, rs.RS_F32, 1.0), (2050, 4095, 0, 0, rs.RS_F32, 1.0),
+]
+ROW_IDS = [f"{r}x{v}+{p}@{s}-{'f32' if d == rs.RS_F32 else 'bf16'}-T{t}" for r, v, p, s, d, t in ROW_SHAPES]
+
+
 def targets_of(rows, vocab, seed):
     """A token for most rows; some at the ends of the row, some without."""
     y = np.random.default_rng(seed).integers(0, vocab, rows)
@@ -166,6 +178,15 @@ def policy_bounds(exp, z64, old, ref, adv, w, temp, kl):
 @pytest.mark.parametrize("shape", SHAPES, ids=IDS)
 @pytest.mark.parametrize("kl", [0.0, 0.1])
 def test_policy_loss(shape, kl):
+    check_policy(shape, kl)
+
+
+@pytest.mark.parametrize("shape", ROW_SHAPES, ids=ROW_IDS)
+def test_policy_loss_a_workgroup_a_row(shape):
+    check_policy(shape, 0.1)
+
+
+def check_policy(shape, kl):
     rows, vocab, pad, shift, dtype, temp = shape
     log(f"policy_loss {shape} kl={kl}")
     _, z = make_logits(rows, vocab, vocab + pad, dtype, 5, shift)
@@ -506,3 +527,45 @@ def test_rows_behind_32_bit_offsets():
     # r = 1 up to the rounding of old: the token's value is p - 1, the others p
     off = z[live].float().sum(1).abs().max().item()
     assert off < 2.0 ** -8 * 2.0  # half a step on each of values that add up to 2 in size
+
+
+def test_more_rows_than_one_launch_takes():
+    """2^22 + 9 rows of 3 values: the launches are cut into slices or stride
+    over the rows; against torch in binary64, row sums of the gradient 0."""
+    log("more rows than a launch takes")
+    rows, vocab = (1 << 22) + 9, 3
+    g = torch.Generator(device="cuda").manual_seed(2)
+    z = torch.randn(rows, vocab, device="cuda", generator=g)
+    y = torch.randint(-1, vocab, (rows,), device="cuda", generator=g)
+    work, n = work_for(rows, vocab)
+    logp, again = torch.full((rows,), SENT, device="cuda"), torch.full((rows,), SENT, device="cuda")
+    rs.rs_token_logp(z, rs.RS_F32, rows, vocab, vocab, y, logp, work, n)
+    full = torch.log_softmax(z.double(), -1)
+    exp = torch.where(y >= 0, full.gather(1, y.clamp(min=0)[:, None])[:, 0], torch.zeros_like(full[:, 0]))
+    bound = (9 * (3 * 12 + 3) + 4 + 12) * U  # values within 12 of each other
+    assert (logp.double() - exp).abs().max().item() < bound
+    one, d, stats = torch.ones(rows, device="cuda"), torch.full_like(z, SENT), torch.zeros(4, device="cuda")
+    rs.rs_policy_loss(z, rs.RS_F32, rows, vocab, vocab, y, logp, None, one, one, d, vocab, again, stats, work, n)
+    assert (again.double() - exp).abs().max().item() < bound
+    p = full.exp()
+    p[y >= 0] = p[y >= 0].scatter_add(1, y[y >= 0][:, None], -torch.ones_like(p[y >= 0][:, :1]))
+    p[y < 0] = 0
+    # r = exp(logp - its rounding) is off by u |logp|, and the bounds above
+    assert (d.double() - p).abs().max().item() < 2 * bound
+    live = int((y >= 0).sum())
+    assert abs(stats[0].item() + live) <= live * (bound + 2 * U)
+
+
+def test_kl_weight_of_zero_leaves_the_reference_out():
+    log("policy kl_coef 0 with a reference")
+    rows, vocab = 5, 50
+    z = torch.randn(rows, vocab, device="cuda")
+    y = torch.arange(rows, device="cuda")
+    one = torch.ones(rows, device="cuda")
+    work, n = work_for(rows, vocab)
+    a, b = torch.zeros(rows, vocab, device="cuda"), torch.zeros(rows, vocab, device="cuda")
+    s, t = torch.zeros(4, device="cuda"), torch.zeros(4, device="cuda")
+    far = torch.full((rows,), 1e5, device="cuda")  # exp(ref - logp) overflows
+    rs.rs_policy_loss(z, rs.RS_F32, rows, vocab, vocab, y, one, far, one, one, a, vocab, None, s, work, n)
+    rs.rs_policy_loss(z, rs.RS_F32, rows, vocab, vocab, y, one, None, one, one, b, vocab, None, t, work, n)
+    assert torch.equal(a, b) and s[0] == t[0] and torch.isfinite(s[:2]).all()
