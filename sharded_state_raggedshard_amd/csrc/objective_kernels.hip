@@ -554,11 +554,22 @@ __global__ __launch_bounds__(NT, 4) void policy_row_kernel(LogitRows a, PolicyTe
     grad_part<T, NT>(z, to, ps, Part{kHeld * NT, ps.n, true}, k, [&] { return gr; });
 }
 
-__global__ __launch_bounds__(1024) void policy_sum_kernel(PolicyTerms t, int64_t rows, float* stats) {
+__global__ __launch_bounds__(1024) void policy_sum_kernel(PolicyTerms t, const double* terms,
+                                                          int64_t n, float* stats) {
     __shared__ double lds[16];
     double sum[3];
-    sum_terms<1024>(t.terms, rows, sum, lds);
+    sum_terms<1024>(terms, n, sum, lds);
     if (threadIdx.x == 0) policy_stats(t, sum, stats);
+}
+
+// Many rows: workgroup b first sums their b-th slice.
+__global__ __launch_bounds__(256) void policy_slice_kernel(PolicyTerms t, int64_t rows, int64_t per) {
+    __shared__ double lds[4];
+    const int64_t r0 = blockIdx.x * per, left = rows - r0;
+    double sum[3];
+    sum_terms<256>(t.terms + 3 * r0, left < per ? left : per, sum, lds);
+    if (threadIdx.x == 0)
+        for (int j = 0; j < 3; ++j) t.slices[3 * blockIdx.x + j] = sum[j];
 }
 
 // ---------------------------------------------------------- preference loss
@@ -730,6 +741,9 @@ int policy_row_threads(int64_t rows, int64_t bytes) {
     return rows >= 2048 && bytes <= (16 << 10) ? 64 : 256;
 }
 
+// Rows whose sums one workgroup adds up in the time of another launch.
+constexpr int64_t kSumRows = 16384;
+
 template <int NT>
 hipError_t launch_policy_rows(const LogitRows& a, const PolicyTerms& t, void* d, int64_t ldd,
                               float* logp, hipStream_t s) {
@@ -793,7 +807,17 @@ hipError_t launch_policy(const LogitRows& a, const PolicyTerms& t, void* d, int6
                    : nt == 512 ? launch_policy_rows<512>(a, t, d, ldd, logp, s)
                                : launch_policy_rows<1024>(a, t, d, ldd, logp, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(policy_sum_kernel, dim3(1), dim3(1024), 0, s, t, a.rows, stats);
+    const double* terms = t.terms;
+    int64_t n = a.rows;
+    if (n > kSumRows) {
+        const int64_t per = (n + kTermSlices - 1) / kTermSlices;
+        n = (n + per - 1) / per;
+        hipLaunchKernelGGL(policy_slice_kernel, dim3((unsigned)n), dim3(256), 0, s, t, a.rows, per);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        terms = t.slices;
+    }
+    hipLaunchKernelGGL(policy_sum_kernel, dim3(1), dim3(1024), 0, s, t, terms, n, stats);
     return hipGetLastError();
 }
 

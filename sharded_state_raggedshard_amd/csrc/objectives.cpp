@@ -20,7 +20,7 @@ constexpr int64_t kMaxPairs = int64_t(1) << 21;  // one workgroup each in one la
 // Scratch: row statistics, token logits, the sums of rows or pairs; for the
 // preference loss also marks and what the rows' gradients take.
 struct Scratch {
-    size_t stat = 0, token = 0, mark = 0, grad = 0, terms = 0, bytes = 0;
+    size_t stat = 0, token = 0, mark = 0, grad = 0, terms = 0, slices = 0, bytes = 0;
 };
 
 Scratch scratch_of(int64_t rows, int64_t vocab, int64_t n_seq) {
@@ -34,6 +34,7 @@ Scratch scratch_of(int64_t rows, int64_t vocab, int64_t n_seq) {
     s.stat = take(size_t(rows) * rs::stat_parts(rows, vocab) * sizeof(rs::RowStat));
     s.token = take(size_t(rows) * sizeof(float));
     s.terms = take(size_t(std::max(rows, n_seq / 2)) * 3 * sizeof(double));
+    s.slices = take(size_t(rs::kTermSlices) * 3 * sizeof(double));
     if (n_seq > 0) {
         s.mark = take(size_t(rows) * sizeof(int32_t));
         s.grad = take(size_t(rows) * sizeof(rs::GradRow));
@@ -141,6 +142,7 @@ rs_status rs_policy_loss(const void* d_logits, int32_t dtype, int64_t rows, int6
     t.hi = 1.0 + hp->clip_high;
     t.kl_coef = hp->kl_coef;
     t.terms = reinterpret_cast<double*>(static_cast<uint8_t*>(d_work) + sc.terms);
+    t.slices = reinterpret_cast<double*>(static_cast<uint8_t*>(d_work) + sc.slices);
     hipError_t e = rs::launch_policy(a, t, d_dlogits, ldd, d_logp, d_stats, as_stream(stream));
     if (e != hipSuccess) return hip_fail(e, "policy_loss launch");
     return RS_OK;

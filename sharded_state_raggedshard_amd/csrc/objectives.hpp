@@ -9,6 +9,7 @@
 namespace rs {
 
 constexpr int64_t kMaxVocab = int64_t(1) << 24;
+constexpr int64_t kTermSlices = 512;  // slices of rows whose sums come first
 
 // log2(e) / temperature as hi + lo, hi rounded towards 0 and lo > 0 (so that
 // -inf times either is -inf).
@@ -48,7 +49,8 @@ struct PolicyTerms {
     const float* ref_logp;  // nullable: no KL term
     const float* advantage;
     double lo, hi, kl_coef;  // the ratio's bounds
-    double* terms;           // scratch: three sums per row
+    double* terms;           // scratch: three sums per row, then per slice
+    double* slices;
 };
 
 struct PreferenceTerms {
