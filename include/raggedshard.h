@@ -33,7 +33,8 @@
  *     the host before any launch, and a failed check launches nothing.
  *     rs_last_error() returns a thread-local message for the last non-OK
  *     status of the calling thread.
- *   - Device pointers must be 16-byte aligned.
+ *   - Device pointers must be 16-byte aligned (the training objectives state
+ *     their own rule).
  *   - Concurrency: calls on distinct plans are independent.  Device calls on
  *     one plan share that plan's workspace scratch and must be ordered on
  *     one stream (or synchronised by the caller); the one exception,

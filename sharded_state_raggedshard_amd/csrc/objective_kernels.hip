@@ -493,6 +493,10 @@ __global__ __launch_bounds__(NT) void policy_grad_kernel(LogitRows a, PolicyTerm
 // 3.68 GB it cannot do without).  16 held (spills) 747, 8 held 750.  Holding
 // all of a row in 1024 threads and loading the next row while storing took
 // 920: four waves a SIMD in step leave the memory idle while they sum.
+// Neither 9 more pieces a thread in LDS (685, but 64000-value rows 186 ->
+// 204) nor a quarter fewer instructions (694) change it: what bounds it is
+// how the memory takes 512 rows read and written side by side (one linear
+// sweep, as the preference gradient's, reaches 6.2 TB/s).
 constexpr int kHeld = 12;
 
 template <typename T, int NT>
