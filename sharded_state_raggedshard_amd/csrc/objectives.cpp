@@ -104,6 +104,8 @@ rs_status rs_token_logp(const void* d_logits, int32_t dtype, int64_t rows, int64
     if (st != RS_OK) return st;
     if (rows > 0 && !d_logp) return fail(RS_EINVAL, "NULL argument");
     if (!aligned(d_logp, 4) || !aligned(d_lse, 4)) return fail(RS_EINVAL, "misaligned pointer");
+    st = check_apart({d_logp, rows}, {{d_lse, rows}});
+    if (st != RS_OK) return st;
     hipError_t e = rs::launch_token_logp(a, d_logp, d_lse, as_stream(stream));
     if (e != hipSuccess) return hip_fail(e, "token_logp launch");
     return RS_OK;
@@ -132,6 +134,12 @@ rs_status rs_policy_loss(const void* d_logits, int32_t dtype, int64_t rows, int6
         !aligned(d_weight, 4) || !aligned(d_logp, 4) || !aligned(d_stats, 4))
         return fail(RS_EINVAL, "misaligned pointer");
     st = check_gradient(d_logits, d_dlogits, dtype, rows, vocab, ld, ldd);
+    if (st != RS_OK) return st;
+    for (const Floats& out : {Floats{d_logp, rows}, Floats{d_stats, 4}}) {
+        st = check_apart(out, {{d_old_logp, rows}, {d_ref_logp, rows}, {d_advantage, rows}, {d_weight, rows}});
+        if (st != RS_OK) return st;
+    }
+    st = check_apart({d_logp, rows}, {{d_stats, 4}});
     if (st != RS_OK) return st;
     a.weight = d_weight;
     rs::PolicyTerms t;
@@ -173,6 +181,12 @@ rs_status rs_preference_loss(const void* d_logits, int32_t dtype, int64_t rows, 
         !aligned(d_seq_logp, 4) || !aligned(d_stats, 4))
         return fail(RS_EINVAL, "misaligned pointer");
     st = check_gradient(d_logits, d_dlogits, dtype, rows, vocab, ld, ldd);
+    if (st != RS_OK) return st;
+    for (const Floats& out : {Floats{d_seq_logp, 2 * n_pairs}, Floats{d_stats, 3}}) {
+        st = check_apart(out, {{d_ref_logp, 2 * n_pairs}, {d_weight, n_pairs}});
+        if (st != RS_OK) return st;
+    }
+    st = check_apart({d_seq_logp, 2 * n_pairs}, {{d_stats, 3}});
     if (st != RS_OK) return st;
     uint8_t* w = static_cast<uint8_t*>(d_work);
     rs::PreferenceTerms t;

@@ -3,6 +3,7 @@
 #pragma once
 #include <hip/hip_runtime_api.h>
 
+#include <initializer_list>
 #include <string>
 
 #include "plan.hpp"
@@ -56,6 +57,24 @@ inline rs_status check_gradient(const void* z, const void* d, int32_t dtype, int
         if (off >= row && off + row <= step) return RS_OK;
     }
     return fail(RS_EINVAL, "the gradient overlaps the logits without being them");
+}
+
+// An array of n binary32 values; NULL takes no room.
+struct Floats {
+    const float* p;
+    int64_t n;
+};
+
+// out must share no value with any of the others: a workgroup may write it
+// while another still reads them.
+inline rs_status check_apart(Floats out, std::initializer_list<Floats> others) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out.p), a1 = a + uintptr_t(out.n) * 4;
+    for (const Floats& o : others) {
+        const uintptr_t b = reinterpret_cast<uintptr_t>(o.p), b1 = b + uintptr_t(o.n) * 4;
+        if (out.p && o.p && a < b1 && b < a1)
+            return fail(RS_EINVAL, "an output overlaps another array");
+    }
+    return RS_OK;
 }
 
 }  // namespace rowcheck

@@ -117,6 +117,31 @@ def test_preference_arguments_are_checked():
         _expect(rs.RS_EINVAL, _pref, **kw)
 
 
+def test_outputs_that_overlap_other_arrays_are_refused():
+    def refused(call, **kw):
+        with pytest.raises(rs.RaggedShardError, match="overlaps another array") as e:
+            call(**kw)
+        assert e.value.status == rs.RS_EINVAL
+
+    far = [P + (i << 20) for i in range(1, 8)]
+    refused(_logp, logp=far[0], lse=far[0])
+    refused(_logp, logp=far[0], lse=far[0] + 4 * 3)  # the last of four rows
+    policy = dict(old_logp=far[0], ref_logp=far[1], advantage=far[2], weight=far[3], logp=far[4],
+                  stats=far[5])
+    for name in ("old_logp", "ref_logp", "advantage", "weight"):
+        for out in ("logp", "stats"):
+            refused(_policy, **{**policy, out: policy[name]})
+            refused(_policy, **{**policy, out: policy[name] + 4 * 3})
+            refused(_policy, **{**policy, out: policy[name] - 4 * 3})
+    refused(_policy, **{**policy, "stats": policy["logp"]})
+    pref = dict(ref_logp=far[0], weight=far[1], seq_logp=far[2], stats=far[3])
+    for name, n in (("ref_logp", 4), ("weight", 2)):
+        for out in ("seq_logp", "stats"):
+            refused(_pref, **{**pref, out: pref[name]})
+            refused(_pref, **{**pref, out: pref[name] + 4 * (n - 1)})
+    refused(_pref, **{**pref, "stats": pref["seq_logp"]})
+
+
 def test_scratch_sizes():
     assert rs.rs_objective_bytes(0, 1, 0) > 0
     a, b = rs.rs_objective_bytes(1000, 32000), rs.rs_objective_bytes(1000, 32000, 8)
