@@ -217,7 +217,8 @@ struct Losses {
 // The exponentials take no shift first: a sum in (2^-10, 2^20) keeps the
 // values that matter within +-14 of 0, where x log2(e) is rounded by less
 // than 2^-20.  If a row of the wave is out of that, or masked, the wave takes
-// its rows again, around the maximum and with selects.
+// its rows again, with selects, and those out of it around their maximum.
+// (A sum of sigmoids is out of it below 2^-10 only, where every x < -6.9.)
 template <int L, int C, bool SIGMOID>
 __device__ __forceinline__ void balance_row(float (&x)[C], const float (&g)[C], float (&acc)[C],
                                             bool live, float c2, Losses& loss) {
@@ -271,6 +272,9 @@ __device__ __forceinline__ void balance_row(float (&x)[C], const float (&g)[C], 
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             p[i] = exp2_fast((x[i] - shift) * kLog2e);
+            // s(x) = e^x (1 - s(x)): a softmax's share alone would be off by
+            // s(x) of itself, up to 2^-10 here
+            if (SIGMOID) p[i] *= w[i];
             sum += p[i];
             gs = __builtin_fmaf(g[i], p[i], gs);
         }
