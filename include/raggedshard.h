@@ -473,9 +473,11 @@ rs_status rs_muon_apply(const rs_muon* muon, int32_t root, float* d_master, cons
  * losses of it follow IEEE arithmetic; NaN or +inf logits give NaN.
  *
  * d_work: device scratch of at least the bytes the matching _bytes function
- * gives, 16-byte aligned.  It carries nothing from call to call and needs no
- * initialisation; calls that share one must be ordered by the caller.  The
- * calls only launch kernels on `stream` (capturable in a HIP graph). */
+ * gives, 16-byte aligned.  The bytes of a size serve every smaller one (fewer
+ * rows, a shorter vocabulary or fewer experts, fewer sequences).  It carries
+ * nothing from call to call and needs no initialisation; calls that share one
+ * must be ordered by the caller.  The calls only launch kernels on `stream`
+ * (capturable in a HIP graph). */
 
 /* Scratch bytes of rs_token_logp and rs_policy_loss (n_seq = 0) and of
  * rs_preference_loss (n_seq = 2 * n_pairs); 0 for sizes the calls refuse. */

@@ -770,7 +770,8 @@ hipError_t launch_policy_rows(const LogitRows& a, const PolicyTerms& t, void* d,
 
 int32_t stat_parts(int64_t rows, int64_t vocab) {
     int32_t parts = 1;
-    while (rows > 0 && parts < 32 && rows * 2 * parts <= 1024 && vocab >= 2 * parts * 4096) parts *= 2;
+    while (rows > 0 && parts < kMaxParts && rows * 2 * parts <= kSplitItems && vocab >= 2 * parts * 4096)
+        parts *= 2;
     return parts;
 }
 

@@ -23,6 +23,18 @@ struct Scratch {
     size_t stat = 0, token = 0, mark = 0, grad = 0, terms = 0, slices = 0, bytes = 0;
 };
 
+// Statistics of the most demanding call of up to `rows` rows: few rows are
+// split into parts, so they may take more than many (512 rows x 128256 have
+// 1024 parts, 513 rows one each).  A workspace for `rows` serves fewer.
+int64_t stat_room(int64_t rows, int64_t vocab) {
+    int64_t room = rows;
+    for (int32_t parts = 1; parts <= rs::kMaxParts; parts *= 2) {
+        const int64_t r = std::min(rows, rs::kSplitItems / parts);
+        room = std::max(room, r * rs::stat_parts(r, vocab));
+    }
+    return room;
+}
+
 Scratch scratch_of(int64_t rows, int64_t vocab, int64_t n_seq) {
     Scratch s;
     size_t at = 0;
@@ -31,7 +43,7 @@ Scratch scratch_of(int64_t rows, int64_t vocab, int64_t n_seq) {
         at = align256(at + n);
         return p;
     };
-    s.stat = take(size_t(rows) * rs::stat_parts(rows, vocab) * sizeof(rs::RowStat));
+    s.stat = take(size_t(stat_room(rows, vocab)) * sizeof(rs::RowStat));
     s.token = take(size_t(rows) * sizeof(float));
     s.terms = take(size_t(std::max(rows, n_seq / 2)) * 3 * sizeof(double));
     s.slices = take(size_t(rs::kTermSlices) * 3 * sizeof(double));

@@ -67,7 +67,10 @@ struct PreferenceTerms {
     double* terms;
 };
 
-// Parts a row is split into for its statistics.
+// Parts a row is split into for its statistics: a power of two up to
+// kMaxParts, no more than kSplitItems parts of all rows together.
+constexpr int32_t kMaxParts = 32;
+constexpr int64_t kSplitItems = 1024;
 int32_t stat_parts(int64_t rows, int64_t vocab);
 
 hipError_t launch_token_logp(const LogitRows& a, float* logp, float* lse, hipStream_t s);

@@ -21,11 +21,14 @@ struct Scratch {
 };
 
 Scratch scratch_of(int64_t rows, int32_t experts, int64_t n_seq) {
-    const rs::RouterChunks c = rs::router_chunks(rows, n_seq);
+    // room for the most chunks that up to `rows` rows are cut into, so that a
+    // workspace for `rows` serves fewer (32768 rows are 1024 chunks, 34000
+    // only 1000)
+    const int64_t chunks = std::min(rows, rs::kMaxChunks);
     Scratch s;
     s.part = align256(size_t(n_seq) * sizeof(int32_t));
-    s.loss = s.part + align256(size_t(c.n + n_seq) * size_t(experts) * sizeof(float));
-    s.bytes = s.loss + align256(size_t(c.n) * 2 * sizeof(double));
+    s.loss = s.part + align256(size_t(chunks + n_seq) * size_t(experts) * sizeof(float));
+    s.bytes = s.loss + align256(size_t(chunks) * 2 * sizeof(double));
     return s;
 }
 

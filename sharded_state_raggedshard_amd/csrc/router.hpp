@@ -33,7 +33,9 @@ struct RouterBalance {
     double* loss;
 };
 
-// Row chunks of the main kernel (one workgroup each) and their length.
+// Row chunks of the main kernel (one workgroup each, at most kMaxChunks) and
+// their length.
+constexpr int64_t kMaxChunks = 1024;
 struct RouterChunks {
     int64_t n, rows;
 };

@@ -568,7 +568,7 @@ RouterChunks router_chunks(int64_t rows, int64_t n_seq) {
     // (40 rows in 60 sequences: 114 us in two chunks)
     RouterChunks c;
     const int64_t least = std::min<int64_t>(32, std::max<int64_t>(1, rows / n_seq));
-    c.rows = std::max<int64_t>(least, (rows + 1023) / 1024);
+    c.rows = std::max<int64_t>(least, (rows + kMaxChunks - 1) / kMaxChunks);
     c.n = (rows + c.rows - 1) / c.rows;
     return c;
 }
