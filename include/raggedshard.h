@@ -456,8 +456,8 @@ rs_status rs_muon_apply(const rs_muon* muon, int32_t root, float* d_master, cons
  * offset t * ld, dtype RS_F32 or RS_BF16; the columns behind a row's values
  * are neither read nor written.  d_dlogits has the same dtype and its own
  * row stride ldd; it may be d_logits itself with ldd = ld (in place), and is
- * otherwise disjoint from it; NULL asks for the loss alone.  No other output
- * overlaps an input or another output (RS_EINVAL among the fp32 arrays).
+ * otherwise disjoint from it; NULL asks for the loss alone.  No other output,
+ * nor the scratch, overlaps an input or another output (RS_EINVAL).
  * Logits, their gradients and all other arrays need the alignment of their
  * elements only.
  * Exponentials are binary32, sums over a row binary64 (of up to 8 terms added

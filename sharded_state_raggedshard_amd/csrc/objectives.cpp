@@ -93,6 +93,11 @@ rs_status fill_rows(const void* z, int32_t dtype, int64_t rows, int64_t vocab, i
     return RS_OK;
 }
 
+Extent logits_of(const rs::LogitRows& a) { return matrix(a.z, a.rows, a.vocab, a.ld, a.f32 ? 4 : 2); }
+Extent gradient_of(const rs::LogitRows& a, const void* d, int64_t ldd) {
+    return matrix(d, a.rows, a.vocab, ldd, a.f32 ? 4 : 2);
+}
+
 }  // namespace
 
 extern "C" {
@@ -116,7 +121,8 @@ rs_status rs_token_logp(const void* d_logits, int32_t dtype, int64_t rows, int64
     if (st != RS_OK) return st;
     if (rows > 0 && !d_logp) return fail(RS_EINVAL, "NULL argument");
     if (!aligned(d_logp, 4) || !aligned(d_lse, 4)) return fail(RS_EINVAL, "misaligned pointer");
-    st = check_apart({d_logp, rows}, {{d_lse, rows}});
+    const Extent scratch{d_work, int64_t(sc.bytes)};
+    st = check_apart({floats(d_logp, rows), floats(d_lse, rows), scratch}, {logits_of(a), longs(d_target, rows)});
     if (st != RS_OK) return st;
     hipError_t e = rs::launch_token_logp(a, d_logp, d_lse, as_stream(stream));
     if (e != hipSuccess) return hip_fail(e, "token_logp launch");
@@ -147,11 +153,12 @@ rs_status rs_policy_loss(const void* d_logits, int32_t dtype, int64_t rows, int6
         return fail(RS_EINVAL, "misaligned pointer");
     st = check_gradient(d_logits, d_dlogits, dtype, rows, vocab, ld, ldd);
     if (st != RS_OK) return st;
-    for (const Floats& out : {Floats{d_logp, rows}, Floats{d_stats, 4}}) {
-        st = check_apart(out, {{d_old_logp, rows}, {d_ref_logp, rows}, {d_advantage, rows}, {d_weight, rows}});
-        if (st != RS_OK) return st;
-    }
-    st = check_apart({d_logp, rows}, {{d_stats, 4}});
+    const Extent logp = floats(d_logp, rows), stats = floats(d_stats, 4);
+    const Extent scratch{d_work, int64_t(sc.bytes)};
+    st = check_apart({logp, stats, scratch, gradient_of(a, d_dlogits, ldd)},
+                     {longs(d_target, rows), floats(d_old_logp, rows), floats(d_ref_logp, rows),
+                      floats(d_advantage, rows), floats(d_weight, rows)});
+    if (st == RS_OK) st = check_apart({logp, stats, scratch}, {logits_of(a)});
     if (st != RS_OK) return st;
     a.weight = d_weight;
     rs::PolicyTerms t;
@@ -194,11 +201,12 @@ rs_status rs_preference_loss(const void* d_logits, int32_t dtype, int64_t rows, 
         return fail(RS_EINVAL, "misaligned pointer");
     st = check_gradient(d_logits, d_dlogits, dtype, rows, vocab, ld, ldd);
     if (st != RS_OK) return st;
-    for (const Floats& out : {Floats{d_seq_logp, 2 * n_pairs}, Floats{d_stats, 3}}) {
-        st = check_apart(out, {{d_ref_logp, 2 * n_pairs}, {d_weight, n_pairs}});
-        if (st != RS_OK) return st;
-    }
-    st = check_apart({d_seq_logp, 2 * n_pairs}, {{d_stats, 3}});
+    const Extent seq_logp = floats(d_seq_logp, 2 * n_pairs), stats = floats(d_stats, 3);
+    const Extent scratch{d_work, int64_t(sc.bytes)};
+    st = check_apart({seq_logp, stats, scratch, gradient_of(a, d_dlogits, ldd)},
+                     {longs(d_target, rows), longs(d_start, 2 * n_pairs + 1), floats(d_ref_logp, 2 * n_pairs),
+                      floats(d_weight, n_pairs)});
+    if (st == RS_OK) st = check_apart({seq_logp, stats, scratch}, {logits_of(a)});
     if (st != RS_OK) return st;
     uint8_t* w = static_cast<uint8_t*>(d_work);
     rs::PreferenceTerms t;

@@ -80,6 +80,13 @@ rs_status rs_router_balance(const void* d_logits, int32_t dtype, int64_t rows, i
     if (bytes < sc.bytes)
         return fail(RS_ENOMEM, "workspace of " + std::to_string(bytes) + " bytes; the call needs " +
                                    std::to_string(sc.bytes));
+    const int64_t size = dtype == RS_F32 ? 4 : 2;
+    const Extent counts{d_counts, n_seq * experts * 4}, mean = floats(d_mean_prob, n_seq * experts);
+    const Extent stats = floats(d_stats, 2), scratch{d_work, int64_t(sc.bytes)};
+    st = check_apart({counts, mean, stats, scratch, matrix(d_dlogits, rows, experts, ldd, size)},
+                     {matrix(d_topk, rows, k, ldk, 8), Extent{d_mask, rows}, longs(d_start, n_seq + 1)});
+    if (st == RS_OK) st = check_apart({counts, mean, stats, scratch}, {matrix(d_logits, rows, experts, ld, size)});
+    if (st != RS_OK) return st;
     uint8_t* w = static_cast<uint8_t*>(d_work);
     rs::RouterBalance a;
     a.z = d_logits;

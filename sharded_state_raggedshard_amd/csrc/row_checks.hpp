@@ -37,6 +37,37 @@ inline rs_status check_logits(const void* z, int32_t dtype, int64_t rows, int64_
     return RS_OK;
 }
 
+// Bytes of an array: `rows` pieces of `bytes`, `step` apart.  A NULL pointer
+// takes no room.
+struct Extent {
+    const void* p;
+    int64_t bytes;
+    int64_t rows = 1, step = 0;
+};
+inline Extent floats(const float* p, int64_t n) { return {p, n * 4}; }
+inline Extent longs(const int64_t* p, int64_t n) { return {p, n * 8}; }
+inline Extent matrix(const void* p, int64_t rows, int64_t width, int64_t ld, int64_t size) {
+    return {p, width * size, rows, rows > 1 && p ? ld * size : 0};
+}
+
+// Whether two arrays share no byte; pieces of different steps, both with
+// gaps, count as sharing one where their ranges meet.
+inline bool apart(const Extent& x, const Extent& y) {
+    if (!x.p || !y.p || x.bytes == 0 || y.bytes == 0 || x.rows == 0 || y.rows == 0) return true;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    const uintptr_t a1 = a + uintptr_t((x.rows - 1) * x.step + x.bytes);
+    const uintptr_t b1 = b + uintptr_t((y.rows - 1) * y.step + y.bytes);
+    if (a1 <= b || b1 <= a) return true;
+    if (x.rows == 1 && y.rows == 1) return false;
+    if (x.rows == 1) return apart(y, x);
+    const uintptr_t step = uintptr_t(x.step);
+    if (y.rows == 1 && b < a) return false;  // y reaches into x's first piece
+    if (y.rows != 1 && y.step != x.step) return false;
+    // y between two pieces of x, or each piece of y between two of x
+    const uintptr_t off = b >= a ? (b - a) % step : (step - (a - b) % step) % step;
+    return off >= uintptr_t(x.bytes) && off + uintptr_t(y.bytes) <= step;
+}
+
 // d must be z with the same stride, or share no element with it.
 inline rs_status check_gradient(const void* z, const void* d, int32_t dtype, int64_t rows, int64_t width,
                          int64_t ld, int64_t ldd) {
@@ -45,34 +76,19 @@ inline rs_status check_gradient(const void* z, const void* d, int32_t dtype, int
     if (!aligned(d, size_t(size))) return fail(RS_EINVAL, "misaligned pointer");
     if (ldd < width) return fail(RS_EINVAL, "row stride below the row's length");
     if (rows > kMaxElems / ldd) return fail(RS_EOVERFLOW, "rows * ldd beyond 2^50 elements");
-    if (rows == 0) return RS_OK;
-    const uintptr_t z0 = reinterpret_cast<uintptr_t>(z), d0 = reinterpret_cast<uintptr_t>(d);
-    const uintptr_t z1 = z0 + uintptr_t(((rows - 1) * ld + width) * size);
-    const uintptr_t d1 = d0 + uintptr_t(((rows - 1) * ldd + width) * size);
-    if (d1 <= z0 || z1 <= d0) return RS_OK;
-    if (ld == ldd && d0 == z0) return RS_OK;
-    if (ld == ldd) {  // columns of one array, side by side
-        const uintptr_t step = uintptr_t(ld * size), row = uintptr_t(width * size);
-        const uintptr_t off = d0 >= z0 ? (d0 - z0) % step : (step - (z0 - d0) % step) % step;
-        if (off >= row && off + row <= step) return RS_OK;
-    }
+    if (d == z && ld == ldd) return RS_OK;
+    if (apart(matrix(z, rows, width, ld, size), matrix(d, rows, width, ldd, size))) return RS_OK;
     return fail(RS_EINVAL, "the gradient overlaps the logits without being them");
 }
 
-// An array of n binary32 values; NULL takes no room.
-struct Floats {
-    const float* p;
-    int64_t n;
-};
-
-// out must share no value with any of the others: a workgroup may write it
-// while another still reads them.
-inline rs_status check_apart(Floats out, std::initializer_list<Floats> others) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(out.p), a1 = a + uintptr_t(out.n) * 4;
-    for (const Floats& o : others) {
-        const uintptr_t b = reinterpret_cast<uintptr_t>(o.p), b1 = b + uintptr_t(o.n) * 4;
-        if (out.p && o.p && a < b1 && b < a1)
-            return fail(RS_EINVAL, "an output overlaps another array");
+// No output shares a byte with an input or another output: a workgroup may
+// write it while another still reads the others.
+inline rs_status check_apart(std::initializer_list<Extent> outputs, std::initializer_list<Extent> inputs) {
+    for (const Extent* out = outputs.begin(); out != outputs.end(); ++out) {
+        for (const Extent* other = out + 1; other != outputs.end(); ++other)
+            if (!apart(*out, *other)) return fail(RS_EINVAL, "an output overlaps another array");
+        for (const Extent& in : inputs)
+            if (!apart(*out, in)) return fail(RS_EINVAL, "an output overlaps another array");
     }
     return RS_OK;
 }
