@@ -24,7 +24,7 @@ Scratch scratch_of(int64_t rows, int32_t experts, int64_t n_seq) {
     // room for the most chunks that up to `rows` rows are cut into, so that a
     // workspace for `rows` serves fewer (32768 rows are 1024 chunks, 34000
     // only 1000)
-    const int64_t chunks = std::min(rows, rs::kMaxChunks);
+    const int64_t chunks = rs::router_chunk_room(rows, experts);
     Scratch s;
     s.part = align256(size_t(n_seq) * sizeof(int32_t));
     s.loss = s.part + align256(size_t(chunks + n_seq) * size_t(experts) * sizeof(float));

@@ -33,13 +33,14 @@ struct RouterBalance {
     double* loss;
 };
 
-// Row chunks of the main kernel (one workgroup each, at most kMaxChunks) and
-// their length.
-constexpr int64_t kMaxChunks = 1024;
+// Row chunks of the main kernel (one workgroup each) and their length; the
+// most chunks that up to `rows` rows are cut into.
+constexpr int64_t kRoundChunks = 1024;
 struct RouterChunks {
     int64_t n, rows;
 };
-RouterChunks router_chunks(int64_t rows, int64_t n_seq);
+RouterChunks router_chunks(int64_t rows, int32_t experts, int64_t n_seq);
+int64_t router_chunk_room(int64_t rows, int32_t experts);
 
 hipError_t launch_router_balance(const RouterBalance& a, hipStream_t s);
 

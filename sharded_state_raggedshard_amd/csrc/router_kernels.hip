@@ -513,6 +513,17 @@ int lanes_of(int pieces) {
     return l;
 }
 
+// Rows of a chunk: a group of lanes adds up at most 64 rows' shares in
+// binary32 (the lanes of binary32 rows; bf16 rows take half as many), so that
+// a mean's error does not grow with the rows: in chunks of one round, 2^26
+// rows of two experts were off by 240 half steps.  More chunks cost little (us,
+// one round / so): 2^20 x 256 bf16 244.2 / 244.5, 2^24 x 8 bf16 366 / 367,
+// 2^20 x 128 binary32 in one sequence 231 / 241 (the last kernel's sums).
+constexpr int kChain = 64;
+int64_t most_chunk_rows(int32_t experts) {
+    return kChain * (kThreads / std::min(64, lanes_of((experts + 3) / 4)));
+}
+
 // One workgroup does everything up to 16 passes over its rows (us, against
 // four launches, in a graph): 96 x 32 binary32 7.3 / 13.9, 256 x 64 13.2 /
 // 14.7, 128 x 128 13.4 / 15.7, 128 x 256 bf16 14.3 / 16.8; 32 passes 21 / 15.
@@ -561,20 +572,26 @@ hipError_t launch_main(const RouterBalance& a, const RouterChunks& c, hipStream_
 
 }  // namespace
 
-RouterChunks router_chunks(int64_t rows, int64_t n_seq) {
+RouterChunks router_chunks(int64_t rows, int32_t experts, int64_t n_seq) {
     // one round of the 1024 workgroups the device holds, not below 32 rows
     // each (with 16, the last kernel's sums take longer than is won), but no
     // more than a sequence: a workgroup takes its sequences one after another
     // (40 rows in 60 sequences: 114 us in two chunks)
     RouterChunks c;
     const int64_t least = std::min<int64_t>(32, std::max<int64_t>(1, rows / n_seq));
-    c.rows = std::max<int64_t>(least, (rows + kMaxChunks - 1) / kMaxChunks);
+    c.rows = std::max<int64_t>(least, (rows + kRoundChunks - 1) / kRoundChunks);
+    c.rows = std::min(c.rows, most_chunk_rows(experts));
     c.n = (rows + c.rows - 1) / c.rows;
     return c;
 }
 
+int64_t router_chunk_room(int64_t rows, int32_t experts) {
+    const int64_t most = most_chunk_rows(experts);
+    return std::max(std::min(rows, kRoundChunks), (rows + most - 1) / most);
+}
+
 hipError_t launch_router_balance(const RouterBalance& a, hipStream_t s) {
-    const RouterChunks c = router_chunks(a.rows, a.n_seq);
+    const RouterChunks c = router_chunks(a.rows, a.experts, a.n_seq);
     if (small_batch(a)) return launch_main(a, c, s);
     const int64_t cells = a.n_seq * a.experts;
     const int64_t zero = (std::max<int64_t>(cells, a.n_seq) + kThreads - 1) / kThreads;
