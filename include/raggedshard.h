@@ -460,10 +460,11 @@ rs_status rs_muon_apply(const rs_muon* muon, int32_t root, float* d_master, cons
  * nor the scratch, overlaps an input or another output (RS_EINVAL).
  * Logits, their gradients and all other arrays need the alignment of their
  * elements only.
- * Exponentials are binary32, sums over a row binary64 (of up to 8 terms added
- * in binary32), and everything per row (logarithm, ratios, losses, their
- * sums) binary64, rounded once to the output type.  Sums are in a fixed
- * order: equal calls give equal bits.
+ * Exponentials are binary32, sums over a row binary64 (of up to 32 terms added
+ * in binary32, in chains of 8; the row's token stands apart from them, so 1 - p
+ * of a nearly certain token keeps its digits), and everything per row
+ * (logarithm, ratios, losses, their sums) binary64, rounded once to the output
+ * type.  Sums are in a fixed order: equal calls give equal bits.
  *
  * A row's token is d_target[t]; a value outside [0, vocab) (-1 by custom)
  * marks a row without a token.  Such a row, a row of weight 0 and a row

@@ -30,14 +30,16 @@ __device__ __forceinline__ float term(float x, float m, ExpScale k) {
     return exp2_fast(__builtin_fmaf(d, k.hi, d * k.lo));
 }
 
-// Maximum and sum, of a thread's share of a row, a part of it or a row.  The
-// sum is binary64: where one term is nearly the whole row, as a trained
-// model's are, a binary32 sum would round away the rest that 1 - p is made
-// of.  It takes the C values of a call at once, added up in binary32 in four
-// chains.
+// Maximum and sum of a thread's share of a row, a part of it or a row; the
+// row's token is in the maximum from the start, but not in the sum.  Its term
+// joins last (row_end()): where it is nearly the whole row, as a trained
+// model's are, any sum with it would round away the rest that 1 - p is made
+// of (a runner-up 17 below, among the values that binary32 adds up with the
+// token, left a gradient of 0).  The sum is binary64; the C values of a call
+// are added up in binary32 in four chains.
 struct MaxSum {
-    float m = kNegInf;
-    double s = 0.0;
+    float m;  // the token's value at first
+    double s;
 
     template <int C>
     __device__ __forceinline__ void take(const float (&x)[C], ExpScale k) {
@@ -96,20 +98,24 @@ __device__ __forceinline__ MaxSum wg_join(MaxSum x, ExpScale k, JoinLds<NT>& lds
     return x;
 }
 
-// What the statistics of a row come to.
+// What the statistics of a row come to, its token among the values.
 struct RowEnd {
     float m;
-    double s;
-    double lse_m;  // log sum exp((z - m) / T)
-    bool empty;    // nothing but -inf
+    double s, rest;  // sums of exp((z - m) / T), `rest` without the token's
+    double lse_m;    // log s
+    bool empty;      // nothing but -inf
 };
 
-__device__ __forceinline__ RowEnd row_end(const MaxSum& x) {
+__device__ __forceinline__ RowEnd row_end(const MaxSum& x, float token, ExpScale k) {
     RowEnd e;
+    const float own = term(token, x.m == kNegInf ? 0.0f : x.m, k);
     e.m = x.m;
-    e.s = x.s;
-    e.empty = x.m == kNegInf && x.s == 0.0;
-    e.lse_m = e.empty ? 0.0 : log(x.s);
+    e.rest = x.s;
+    e.s = x.s + (double)own;
+    e.empty = e.m == kNegInf && e.s == 0.0;
+    // log(1 + rest) of a small rest: 1 + rest has rounded its digits away
+    const bool sure = own == 1.0f && e.rest < 0x1p-20;
+    e.lse_m = e.empty ? 0.0 : sure ? e.rest - 0.5 * e.rest * e.rest : log(e.s);
     return e;
 }
 
@@ -120,7 +126,7 @@ __device__ __forceinline__ RowEnd row_of(const LogitRows& a, int64_t row, ExpSca
         const RowStat q = p[i];
         x.join(q.m, q.s, k);
     }
-    return row_end(x);
+    return row_end(x, a.token[row], k);
 }
 
 __device__ __forceinline__ double logp_of(const RowEnd& e, float token, double scale) {
@@ -174,34 +180,50 @@ __device__ __forceinline__ Part part_of(const T* row, const Pieces<T>& ps, int p
     return Part{a < 0 ? 0 : a < ps.n ? a : ps.n, b < ps.n ? b : ps.n, part == parts - 1};
 }
 
-// Statistics of a part of a row, by the whole workgroup: U loads a thread in
-// flight (the last ones padded with -inf).  ONCE: not read again soon.
+// The values of a part of a row that are taken one by one, a thread each: the
+// edges, and the values beside token y in its piece (from the 33rd thread
+// on), if that is one of [v0, part.v1).  Every thread loads one, the token
+// where it has none, and opens it in value(), after the pieces' loads have
+// begun: waiting for it first took 0.7 us a row.
+template <typename T>
+struct Single {
+    int at, y;
+    T raw;
+    __device__ __forceinline__ Single(const T* z, const Pieces<T>& ps, Part part, int v0, int y) : at(y), y(y) {
+        constexpr int N = Vec<T>::n;
+        const int tid = threadIdx.x, yv = ps.piece(y);
+        if (part.ends && tid < ps.edges) at = ps.edge(tid);
+        if (yv >= v0 && yv < part.v1 && tid >= 32 && tid < 32 + N) at = ps.head + yv * N + tid - 32;
+        raw = z[at];
+    }
+    __device__ __forceinline__ float value() const { return at != y ? Vec<T>::one(raw) : kNegInf; }
+};
+
+// Statistics of a part of a row without the piece of token y and the values
+// that Single takes, by the whole workgroup: U loads a thread in flight
+// (the last ones padded with -inf).  ONCE: not read again soon.
 template <typename T, int NT, bool ONCE>
 __device__ __forceinline__ void take_part(MaxSum& run, const T* z, const Pieces<T>& ps, Part part,
-                                          ExpScale k) {
+                                          int y, ExpScale k) {
     constexpr int N = Vec<T>::n, U = 4;
-    const int tid = threadIdx.x;
     const T* base = z + ps.head;
-    for (int v = part.v0 + tid; v < part.v1; v += U * NT) {
+    const int yv = ps.piece(y);
+    for (int v = part.v0 + threadIdx.x; v < part.v1; v += U * NT) {
         u32x4 w[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             w[u] = Vec<T>::lowest();
             const int at = v + u * NT;
-            if (at < part.v1) w[u] = ONCE ? load16_once(base + at * N) : load16(base + at * N);
+            if (at < part.v1 && at != yv) w[u] = ONCE ? load16_once(base + at * N) : load16(base + at * N);
         }
         float x[U * N];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float y[N];
-            Vec<T>::open(w[u], y);
+            float f[N];
+            Vec<T>::open(w[u], f);
 #pragma unroll
-            for (int i = 0; i < N; ++i) x[u * N + i] = y[i];
+            for (int i = 0; i < N; ++i) x[u * N + i] = f[i];
         }
-        run.take(x, k);
-    }
-    if (part.ends && tid < ps.edges) {
-        const float x[1] = {Vec<T>::one(z[ps.edge(tid)])};
         run.take(x, k);
     }
 }
@@ -250,17 +272,21 @@ __global__ __launch_bounds__(NT) void row_stats_kernel(LogitRows a, PreferenceTe
             continue;
         }
         const T* z = static_cast<const T*>(a.z) + row * a.ld;
-        const float token = Vec<T>::one(z[a.target[row]]);
+        const int y = (int)a.target[row];
+        const float token = Vec<T>::one(z[y]);
         const Pieces<T> ps(z, a.vocab);
-        MaxSum run;
+        const Part p = part_of(z, ps, part, a.parts);
+        const Single<T> one(z, ps, p, p.v0, y);
+        MaxSum run{token, 0.0};
         if (MODE == STATS_KEEP || (MODE == STATS_MARK && row >= t.kept_from))
-            take_part<T, NT, false>(run, z, ps, part_of(z, ps, part, a.parts), k);
+            take_part<T, NT, false>(run, z, ps, p, y, k);
         else
-            take_part<T, NT, true>(run, z, ps, part_of(z, ps, part, a.parts), k);
+            take_part<T, NT, true>(run, z, ps, p, y, k);
+        if (tid < 64) run.take({one.value()}, k);
         run = wg_join<NT>(run, k, lds);
         if (tid != 0) continue;
         if (MODE == STATS_LOGP) {
-            write_logp(a, row, row_end(run), token, logp, lse);
+            write_logp(a, row, row_end(run, token, k), token, logp, lse);
         } else {
             a.stat[item] = RowStat{run.s, run.m, 0.0f};
             if (part == 0) a.token[row] = token;
@@ -289,7 +315,7 @@ __global__ __launch_bounds__(256) void logp_kernel(LogitRows a, float* logp, flo
     float token = 0.0f;
     if (has_token(a, row)) {
         token = a.token[row];
-        e = row_end(join_parts(a, row, part));
+        e = row_end(join_parts(a, row, part), token, a.k);
     }
     if (part == 0) write_logp(a, row, e, token, logp, lse);
 }
@@ -341,14 +367,12 @@ __device__ __forceinline__ void policy_stats(const PolicyTerms& t, const double 
 // ----------------------------------------------------------- logits gradient
 
 // What the gradient of a row, cs ([i = y] - p_i), takes: f = -cs / s and the
-// token's own value cs (1 - p), where 1 - p comes from the binary64 sum, as
-// next to p = 1 it is all that is left.
-__device__ __forceinline__ GradRow grad_row(const RowEnd& e, double cs, int64_t y, float token,
-                                            ExpScale k) {
+// token's own value cs (1 - p), where 1 - p is the sum of the others over all.
+__device__ __forceinline__ GradRow grad_row(const RowEnd& e, double cs, int64_t y) {
     GradRow g;
     g.m = e.m;
     g.f = (float)(-cs / e.s);
-    g.own = (float)(cs * ((e.s - (double)term(token, e.m, k)) / e.s));
+    g.own = (float)(cs * (e.rest / e.s));
     g.y = (int32_t)y;
     return g;
 }
@@ -438,7 +462,7 @@ __global__ __launch_bounds__(NT) void policy_grad_kernel(LogitRows a, PolicyTerm
         PolicyRow p;
         if (row < a.rows) {
             const float token = a.token[row];
-            MaxSum x;
+            MaxSum x{token, 0.0};
             if (sub * per < a.parts) {
                 const RowStat* q = a.stat + row * a.parts + sub * per;
                 x = MaxSum{q[0].m, q[0].s};
@@ -446,7 +470,7 @@ __global__ __launch_bounds__(NT) void policy_grad_kernel(LogitRows a, PolicyTerm
             }
             x.join(__shfl_xor(x.m, 1, 64), __shfl_xor(x.s, 1, 64), k);
             x.join(__shfl_xor(x.m, 2, 64), __shfl_xor(x.s, 2, 64), k);
-            if (sub == 0 && has_token(a, row)) p = policy_row(a, t, row, row_end(x), token);
+            if (sub == 0 && has_token(a, row)) p = policy_row(a, t, row, row_end(x, token, k), token);
             if (sub == 0 && logp) logp[row] = (float)p.logp;
         }
         const double pg = p.pg, kl = p.kl, cl = p.clipped;
@@ -465,14 +489,11 @@ __global__ __launch_bounds__(NT) void policy_grad_kernel(LogitRows a, PolicyTerm
         return;
     }
     grad_part<T, NT>(z, to, ps, part, k, [&] {
-        const RowEnd e = row_end(join_parts(a, row, tid % a.parts));
+        const float token = a.token[row];
+        const RowEnd e = row_end(join_parts(a, row, tid % a.parts), token, k);
         if (tid == 0) {
             g = GradRow{0.0f, 0.0f, 0.0f, -1};  // a row of nothing but -inf: zeros, no token
-            if (!e.empty) {
-                const float token = a.token[row];
-                g = grad_row(e, policy_row(a, t, row, e, token).coef * a.scale, a.target[row],
-                             token, k);
-            }
+            if (!e.empty) g = grad_row(e, policy_row(a, t, row, e, token).coef * a.scale, a.target[row]);
         }
         __syncthreads();
         return g;
@@ -515,24 +536,29 @@ __global__ __launch_bounds__(NT, 4) void policy_row_kernel(LogitRows a, PolicyTe
     e.empty = true;
     u32x4 w[kHeld];
     if (has_token(a, row)) {
-        const float token = Vec<T>::one(z[a.target[row]]);
+        const int y = (int)a.target[row];
+        const float token = Vec<T>::one(z[y]);
 #pragma unroll
         for (int j = 0; j < kHeld; ++j)
             if (j * NT + tid < ps.n) w[j] = load16_once(z + ps.head + (j * NT + tid) * N);
-        MaxSum run;
+        const Part rest{kHeld * NT, ps.n, true};
+        const Single<T> one(z, ps, rest, 0, y);
+        const int yv = ps.piece(y);
+        MaxSum run{token, 0.0};
 #pragma unroll
         for (int j = 0; j < kHeld; ++j) {
-            if (j * NT + tid < ps.n) {
+            if (j * NT + tid < ps.n && j * NT + tid != yv) {
                 float x[N];
                 Vec<T>::open(w[j], x);
                 run.take(x, k);
             }
         }
-        take_part<T, NT, false>(run, z, ps, Part{kHeld * NT, ps.n, true}, k);
-        e = row_end(wg_join<NT>(run, k, lds));
+        take_part<T, NT, false>(run, z, ps, rest, y, k);
+        if (tid < 64) run.take({one.value()}, k);
+        e = row_end(wg_join<NT>(run, k, lds), token, k);
         if (tid == 0 && !e.empty) {
             const PolicyRow p = policy_row(a, t, row, e, token);
-            g = grad_row(e, p.coef * a.scale, a.target[row], token, k);
+            g = grad_row(e, p.coef * a.scale, y);
             t.terms[3 * row] = p.pg;
             t.terms[3 * row + 1] = p.kl;
             t.terms[3 * row + 2] = p.clipped;
@@ -661,7 +687,7 @@ __global__ __launch_bounds__(NT) void pair_kernel(LogitRows a, PreferenceTerms t
     for (int64_t row = r0 + at; row < r1; row += HALF) {
         if (t.mark[row] != MARK_TOKEN) continue;
         const RowEnd e = row == r0 + at ? first : row_of(a, row, k);
-        t.grad[row] = grad_row(e, cs, a.target[row], a.token[row], k);
+        t.grad[row] = grad_row(e, cs, a.target[row]);
     }
 }
 
