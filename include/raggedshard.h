@@ -464,14 +464,16 @@ rs_status rs_muon_apply(const rs_muon* muon, int32_t root, float* d_master, cons
  * in binary32, in chains of 8; the row's token stands apart from them, so 1 - p
  * of a nearly certain token keeps its digits), and everything per row
  * (logarithm, ratios, losses, their sums) binary64, rounded once to the output
- * type.  Sums are in a fixed order: equal calls give equal bits.
+ * type (rs_router_balance has its own rule).  Sums are in a fixed order: equal
+ * calls give equal bits.
  *
  * A row's token is d_target[t]; a value outside [0, vocab) (-1 by custom)
  * marks a row without a token.  Such a row, a row of weight 0 and a row
  * whose logits are all -inf take no part: nothing of theirs that is not
  * finite reaches a result, their logp is 0 and their gradient row is 0.
  * A token whose own logit is -inf in a row with others has logp -inf, and
- * losses of it follow IEEE arithmetic; NaN or +inf logits give NaN.
+ * losses of it follow IEEE arithmetic; NaN or +inf logits give NaN (a router's
+ * sigmoid scores: s(+inf) = 1).
  *
  * d_work: device scratch of at least the bytes the matching _bytes function
  * gives, 16-byte aligned.  The bytes of a size serve every smaller one (fewer
@@ -583,6 +585,9 @@ size_t rs_router_balance_bytes(int64_t rows, int32_t experts, int64_t n_seq);
  *   loss = balance_coef sum_e f_e P_e + z_coef sum_t lse_t^2 / n,
  * summed over the sequences (fold a mean over them into the coefficients).
  * The counts pass no gradient; d_dlogits (nullable) is dloss/dz as dtype.
+ * A row's exponentials (off by up to (1.3 x + 3) 2^-24 of themselves, x = |z| or,
+ * in rows far from 0, max z - z), sums, quotients and logarithm are binary32;
+ * sums over rows are binary64, of up to 64 rows' binary32 sums each.
  * A row whose logits are all -inf has p = 0 and gradient 0 but counts
  * in n.  d_counts, d_mean_prob: n_seq x experts (int32, fp32; 0 for a sequence
  * without tokens); d_stats: 2 floats, the balance and the z part of the

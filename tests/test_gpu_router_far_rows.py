@@ -47,3 +47,31 @@ def test_rows_far_below_zero(centre, experts, dtype, score):
     close(np64(stats), exp["stats"], tol_s, "stats")
     close(np64(d).ravel(), exp["dlogits"].ravel(),
           (tol_d + HALF[dtype] * np.abs(exp["dlogits"]) + 1e-37).ravel(), "dlogits")
+
+
+@pytest.mark.parametrize("dtype", [rs.RS_F32, rs.RS_BF16])
+@pytest.mark.parametrize("masked", [False, True])
+def test_infinite_sigmoid_scores(dtype, masked):
+    """s(+inf) = 1, as s(80) is to 115 bits: same shares, no gradient at the
+    expert itself; with a masked row in the wave too (its other way of
+    taking rows)."""
+    log(f"router infinite scores dtype={dtype} masked={masked}")
+    rows, experts, k = 40, 48, 2
+    g = torch.Generator(device="cuda").manual_seed(62)
+    z = torch.randn(rows, experts, device="cuda", generator=g).to(TORCH[dtype])
+    topk = torch.randint(0, experts, (rows, k), device="cuda", generator=g)
+    mask = np.ones(rows, dtype=bool)
+    mask[3::8] = not masked
+    z[1, 5] = z[2, 7] = z[2, 9] = z[30, 0] = 80.0
+    z64 = np64(z)
+    z[z == 80] = float("inf")
+    exp = ob.router_balance(z64, topk.cpu().numpy(), mask, [0, rows], balance_coef=0.3, score=ob.NORMALISED_SIGMOID)
+    d = torch.full((rows, experts), SENT, dtype=TORCH[dtype], device="cuda")
+    counts, mean, stats = run(z, dtype, experts, topk, torch.from_numpy(mask).cuda(), None, d, experts,
+                              score=rs.RS_SCORE_SIGMOID, balance_coef=0.3)
+    tol_d, tol_m, tol_s = bounds(exp, z64, mask, [0, rows], k, 0.3, 0.0, ob.NORMALISED_SIGMOID)
+    close(np64(mean).ravel(), exp["mean_prob"].ravel(), tol_m.ravel(), "mean_prob")
+    close(np64(stats), exp["stats"], tol_s, "stats")
+    close(np64(d).ravel(), exp["dlogits"].ravel(),
+          (tol_d + HALF[dtype] * np.abs(exp["dlogits"]) + 1e-37).ravel(), "dlogits")
+    assert not d[torch.isinf(z)].any()
