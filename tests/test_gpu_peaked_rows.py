@@ -141,3 +141,37 @@ def test_preference_gradient_of_nearly_certain_tokens(shape):
     c = np.repeat(np.concatenate([g, -g]), np.diff(start))
     dc = 0.25 * tol * np.abs(total).max() * 2 + 2.0 ** -48
     check(np64(d), z64, y, temp, c, dc, dtype, "dlogits")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("rows,vocab,dtype", [(6, 1, rs.RS_F32), (6, 9, rs.RS_BF16), (6, 40000, rs.RS_F32),
+                                              (70, 1003, rs.RS_BF16), (300, 40003, rs.RS_BF16)])
+def test_a_token_that_is_not_finite(rows, vocab, dtype, bad):
+    """NaN or +inf at the token itself, among finite and among masked values,
+    makes its row NaN and no other."""
+    log(f"token of {bad} in {rows} x {vocab} dtype={dtype}")
+    z, _, y = peaked(rows, max(vocab, 2), dtype, 1.0, 0, 85)
+    if vocab == 1:
+        z, y = z[:, :1].contiguous(), np.zeros(rows, dtype=y.dtype)
+        z[:] = 1.0
+    yt = torch.from_numpy(y).cuda()
+    zero, one = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    work, n = work_for(rows, vocab)
+
+    def call():
+        d = torch.full((rows, vocab), SENT, dtype=TORCH[dtype], device="cuda")
+        logp, lse, stats = torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda"), torch.zeros(4, device="cuda")
+        rs.rs_token_logp(z, dtype, rows, vocab, vocab, yt, logp, work, n, lse=lse)
+        first = logp.clone()
+        rs.rs_policy_loss(z, dtype, rows, vocab, vocab, yt, zero, None, one, one, d, vocab, logp, stats, work, n)
+        return d, first, lse, logp, stats
+
+    good = call()
+    for t in (2, 3):
+        z[t, int(y[t])] = bad
+    got = call()
+    keep = [t for t in range(rows) if t not in (2, 3)]
+    for g, h in zip(got[:4], good):
+        assert torch.equal(g[keep], h[keep])
+        assert torch.isnan(g[[2, 3]]).all()
+    assert torch.isnan(got[4][:2]).all() and not torch.isnan(good[4]).any()
