@@ -105,6 +105,10 @@ __device__ __forceinline__ double wg_sum(double v, double* lds) {
 
 // Number of the entries start[1 .. n] that are <= row: the wave's 64 probes
 // narrow the range [lo, hi] of the count by a factor 64 a round.
+// One 64-bit min a round, and no more: with a second one the compiler took the
+// first one's condition for both (s_cselect without its own compare, in a
+// uniform loop), and the search returned a wrong sequence.  A change here
+// needs a look at the generated loop and the tests of many short sequences.
 __device__ __forceinline__ int64_t sequence_of(const int64_t* start, int64_t n, int64_t row) {
     const int lane = threadIdx.x & 63;
     int64_t lo = 0, hi = n;
