@@ -511,7 +511,8 @@ __global__ __launch_bounds__(NT) void policy_grad_kernel(LogitRows a, PolicyTerm
 // 6144 of 8192 rows x 128256 bf16, in us: two kernels over all rows 981;
 // nothing held 793 (512 threads); 12 held 743; with the gradient stored past
 // the caches 710, and held pieces read past them 698 (5.3 TB/s of the
-// 3.68 GB it cannot do without).  16 held (spills) 747, 8 held 750.  Holding
+// 3.68 GB it cannot do without); the token apart from the sums, for its
+// 1 - p, takes 1.5 % more.  16 held (spills) 747, 8 held 750.  Holding
 // all of a row in 1024 threads and loading the next row while storing took
 // 920: four waves a SIMD in step leave the memory idle while they sum.
 // Neither 9 more pieces a thread in LDS (685, but 64000-value rows 186 ->

@@ -216,9 +216,11 @@ struct Losses {
 //
 // The exponentials take no shift first: a sum in (2^-10, 2^20) keeps the
 // values that matter within +-14 of 0, where x log2(e) is rounded by less
-// than 2^-20.  If a row of the wave is out of that, or masked, the wave takes
-// its rows again, with selects, and those out of it around their maximum.
-// (A sum of sigmoids is out of it below 2^-10 only, where every x < -6.9.)
+// than 2^-20 (giving that back as a factor 1 + r costs 1 to 3 % of ordinary
+// softmax batches and 14 % of 2^24 x 8: dropped).  If a row of the wave is
+// out of that, or masked, the wave takes its rows again, with selects, and
+// those out of it around their maximum.  (A sum of sigmoids is out of it
+// below 2^-10 only, where every x < -6.9.)
 template <int L, int C, bool SIGMOID>
 __device__ __forceinline__ void balance_row(float (&x)[C], const float (&g)[C], float (&acc)[C],
                                             bool live, float c2, Losses& loss) {
