@@ -355,6 +355,89 @@ rs_status rs_adam8_step_fp8(const rs_plan* plan, int32_t bucket, int32_t rank, f
                             const float* d_grad_scale, uint16_t* d_bf16_out, uint8_t* d_fp8,
                             float* d_fp8_scale, void* stream);
 
+/* ------------------------------------------------ AdamW over many tensors
+ * The step for parameters that no planned buffer holds (norms, biases,
+ * routers, adapters, a head that trains alone): any number of tensors
+ * wherever they lie, each with its own types, moments and hyper-parameters,
+ * updated in place by one launch.  The update is rs_adam8_step's:
+ *   g = float(grad) * s             (s = *d_grad_scale, or 1 if NULL)
+ *   m = b1 m + (1 - b1) g,          v = b2 v + (1 - b2) g g
+ *   theta = theta (1 - lr wd) - (lr / (1 - b1^t)) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+ * in binary32, rounded once to the parameters' type.  Moments are binary32
+ * (RS_STATE_F32), or RS_STATE_INT8: the codes and absmax of rs_adam8_step,
+ * each block `block` consecutive elements (the last may be shorter),
+ *   m = (q_m / 127) amax_m, q_m = rne(m / amax_m * 127),
+ *   v = (q_v / 255) amax_v, q_v = rne(v / amax_v * 255)  (0 if amax 0),
+ * the new parameters coming from the new moments before they are quantised.
+ * Codes and absmax equal rs_adam8_step's bit for bit.  Non-finite gradients
+ * give unspecified values (as there), in their own tensor only. */
+typedef struct rs_adamw rs_adamw; /* opaque, host-owned */
+
+enum { RS_STATE_F32 = 0, RS_STATE_INT8 = 1 };
+
+typedef struct {
+    int64_t numel;    /* >= 0 */
+    int32_t param;    /* RS_F32 or RS_BF16 */
+    int32_t grad;     /* RS_F32 or RS_BF16 */
+    int32_t state;    /* RS_STATE_* */
+    int32_t block;    /* RS_STATE_INT8: a power of two in 64..4096, else 0 */
+    int32_t group;    /* its hyper-parameters' index in rs_adamw_step, 0..15 */
+    int32_t reserved; /* must be 0 */
+} rs_adamw_tensor;
+
+/* A plan over n tensors (host only).  Errors: RS_EINVAL (n < 1, a bad
+ * tensor), RS_EOVERFLOW (numel beyond 2^42, more than 2^31 - 1 pieces of
+ * 4096 elements), RS_ENOMEM. */
+rs_status rs_adamw_plan(const rs_adamw_tensor* tensors, int32_t n, rs_adamw** out);
+
+/* Releases a plan (NULL is allowed).  Does not touch device memory. */
+void rs_adamw_free(rs_adamw* adamw);
+
+/* Device bytes of the workspace: tables and the norm's partial sums. */
+size_t rs_adamw_device_bytes(const rs_adamw* adamw);
+
+/* Copies the work table into the caller's workspace (>= rs_adamw_device_bytes,
+ * 256-byte aligned); the plan keeps the pointer, and what was bound before
+ * has to be bound again.  Synchronises the stream.  Errors: RS_EINVAL,
+ * RS_ENOMEM (too small), RS_EHIP. */
+rs_status rs_adamw_upload(rs_adamw* adamw, void* d_workspace, size_t bytes, void* stream);
+
+/* Where the tensors' arrays are: host arrays of n device pointers each, all
+ * aligned to their elements.  d_m, d_v: binary32 moments, or int8 / uint8
+ * codes; d_amax_m, d_amax_v: ceil(numel / block) floats (read only for
+ * RS_STATE_INT8 tensors; the arrays may be NULL without any); d_bf16_out
+ * (nullable, entries too): bf16_rne of the new binary32 parameters.  An empty
+ * tensor's pointers are not looked at.  No written array shares a byte with
+ * another array (RS_EINVAL).  May be called again, as when gradients move;
+ * a captured call uses what is bound when it is replayed.  Synchronises the
+ * stream.  Errors: RS_EINVAL, RS_ESTATE (not uploaded), RS_ENOMEM, RS_EHIP. */
+rs_status rs_adamw_bind(rs_adamw* adamw, void* const* d_param, const void* const* d_grad,
+                        void* const* d_m, void* const* d_v, float* const* d_amax_m,
+                        float* const* d_amax_v, uint16_t* const* d_bf16_out, void* stream);
+
+/* *d_sumsq = sum of the squares of every gradient element, in binary64 and a
+ * fixed order (NaN / Inf propagate); with d_scale (nullable) the clipping
+ * coefficient for max_norm, as rs_clip_coef.  (Where other gradients count in
+ * the norm, add the sums and call rs_clip_coef.)  Uses the workspace: calls
+ * on one plan must be ordered.  Errors: RS_EINVAL (max_norm not finite and
+ * > 0 with d_scale; an output among the bound arrays), RS_ESTATE, RS_EHIP. */
+rs_status rs_adamw_l2norm_clip(const rs_adamw* adamw, double max_norm, double* d_sumsq,
+                               float* d_scale, void* stream);
+
+/* One step of every tensor: tensor i takes hp[group_i] (n_groups entries, at
+ * least the highest group + 1, at most 16; a captured call keeps them).
+ * Errors: RS_EINVAL (hyper-parameters as rs_adam8_step; d_grad_scale among
+ * the bound arrays), RS_ESTATE, RS_EHIP. */
+rs_status rs_adamw_step(const rs_adamw* adamw, const rs_adam_hparams* hp, int32_t n_groups,
+                        const float* d_grad_scale, void* stream);
+
+/* The moments as values (a checkpoint that does not depend on how they are
+ * kept): tensor after tensor in the given order, without gaps, as dtype
+ * (RS_F32, or RS_BF16 rounded to nearest even).  Either output may be NULL.
+ * Errors: RS_EINVAL (dtype, alignment, an output among the bound arrays or
+ * overlapping the other), RS_ESTATE, RS_EHIP. */
+rs_status rs_adamw_moments(const rs_adamw* adamw, void* d_m, void* d_v, int32_t dtype, void* stream);
+
 /* ------------------------------------------------------- distributed Muon
  * veScale-FSDP page, section "Structure-aware training case study",
  * distributed Muon (Algorithm 2), with the uneven per-device distribution of

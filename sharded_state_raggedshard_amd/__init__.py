@@ -29,6 +29,7 @@ RS_ALIGN_CUT_UNIT = 0x100
 RS_SPLIT_TWO_PASS, RS_SPLIT_COOPERATIVE, RS_SPLIT_ORDERED = 0, 1, 2
 RS_PREF_SIGMOID, RS_PREF_HINGE, RS_PREF_IPO = 0, 1, 2
 RS_SCORE_SOFTMAX, RS_SCORE_SIGMOID = 0, 1
+RS_STATE_F32, RS_STATE_INT8 = 0, 1
 RS_ALL = -1
 
 # every entry point declared in include/raggedshard.h
@@ -44,6 +45,8 @@ EXPORTS = (
     "rs_muon_gather", "rs_muon_orthogonalize", "rs_muon_apply",
     "rs_objective_bytes", "rs_token_logp", "rs_policy_loss", "rs_preference_loss",
     "rs_router_balance_bytes", "rs_router_balance",
+    "rs_adamw_plan", "rs_adamw_free", "rs_adamw_device_bytes", "rs_adamw_upload", "rs_adamw_bind",
+    "rs_adamw_l2norm_clip", "rs_adamw_step", "rs_adamw_moments",
 )
 
 
@@ -80,6 +83,12 @@ class rs_preference_hparams(C.Structure):
 
 class rs_balance_hparams(C.Structure):
     _fields_ = [("balance_coef", C.c_double), ("z_coef", C.c_double), ("score", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
+class rs_adamw_tensor(C.Structure):
+    _fields_ = [("numel", C.c_int64), ("param", C.c_int32), ("grad", C.c_int32),
+                ("state", C.c_int32), ("block", C.c_int32), ("group", C.c_int32),
                 ("reserved", C.c_int32)]
 
 
@@ -148,6 +157,14 @@ def lib() -> C.CDLL:
         "rs_router_balance": ([vp, i32, i64, i32, i64, vp, i32, i64, vp, vp, i64,
                                C.POINTER(rs_balance_hparams), vp, i64, vp, vp, vp, vp,
                                C.c_size_t, vp], C.c_int),
+        "rs_adamw_plan": ([C.POINTER(rs_adamw_tensor), i32, C.POINTER(vp)], C.c_int),
+        "rs_adamw_free": ([vp], None),
+        "rs_adamw_device_bytes": ([vp], C.c_size_t),
+        "rs_adamw_upload": ([vp, vp, C.c_size_t, vp], C.c_int),
+        "rs_adamw_bind": ([vp, *[C.POINTER(vp)] * 7, vp], C.c_int),
+        "rs_adamw_l2norm_clip": ([vp, C.c_double, vp, vp, vp], C.c_int),
+        "rs_adamw_step": ([vp, C.POINTER(rs_adam_hparams), i32, vp, vp], C.c_int),
+        "rs_adamw_moments": ([vp, vp, vp, i32, vp], C.c_int),
         "rs_last_error": ([], C.c_char_p),
         "rs_version": ([], C.c_char_p),
     }
@@ -170,6 +187,17 @@ def _ptr(x) -> Optional[int]:
         return None
     if isinstance(x, int):
         return x
+    return int(x.data_ptr())
+
+
+def _dev(x) -> Optional[int]:
+    """_ptr of a tensor that the current device holds: a launch there with
+    another one's memory, or the host's, could fault."""
+    if x is None or isinstance(x, int):
+        return x
+    import torch
+    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        raise RaggedShardError(RS_EINVAL, f"a tensor on {x.device}, not on the current device")
     return int(x.data_ptr())
 
 
@@ -494,6 +522,61 @@ def rs_router_balance(logits, dtype: int, rows: int, experts: int, ld: int, topk
                                    _stream(stream)))
 
 
+def rs_adamw_plan(tensors: Sequence) -> int:
+    """tensors: (numel, param dtype, grad dtype, RS_STATE_*, block, group) each."""
+    arr = (rs_adamw_tensor * len(tensors))(*[rs_adamw_tensor(*map(int, t), 0) for t in tensors])
+    h = C.c_void_p()
+    _check(lib().rs_adamw_plan(arr, len(tensors), C.byref(h)))
+    return h.value
+
+
+def rs_adamw_free(adamw: int) -> None:
+    lib().rs_adamw_free(adamw)
+
+
+def rs_adamw_device_bytes(adamw: int) -> int:
+    n = lib().rs_adamw_device_bytes(adamw)
+    if n == 0:
+        raise RaggedShardError(RS_EINVAL, lib().rs_last_error().decode())
+    return int(n)
+
+
+def rs_adamw_upload(adamw: int, workspace, nbytes: int, stream=None) -> None:
+    _check(lib().rs_adamw_upload(adamw, _dev(workspace), nbytes, _stream(stream)))
+
+
+def rs_adamw_bind(adamw: int, params: Sequence, grads: Sequence, m: Sequence, v: Sequence,
+                  amax_m: Optional[Sequence] = None, amax_v: Optional[Sequence] = None,
+                  bf16_out: Optional[Sequence] = None, stream=None) -> None:
+    """One entry per tensor in each list; amax lists (entries of binary32
+    moments None) and bf16_out (entries may be None) may be None."""
+    def table(xs):
+        if xs is None:
+            return None
+        if len(xs) != len(params):
+            raise ValueError("the lists differ in length")
+        return (C.c_void_p * len(xs))(*[_dev(x) for x in xs])
+    _check(lib().rs_adamw_bind(adamw, *[table(x) for x in (params, grads, m, v, amax_m, amax_v,
+                                                           bf16_out)], _stream(stream)))
+
+
+def rs_adamw_l2norm_clip(adamw: int, max_norm: float, sumsq, scale=None, stream=None) -> None:
+    _check(lib().rs_adamw_l2norm_clip(adamw, max_norm, _dev(sumsq), _dev(scale), _stream(stream)))
+
+
+def rs_adamw_step(adamw: int, hparams: Sequence, grad_scale=None, stream=None) -> None:
+    """hparams: rs_adam_hparams, or dicts of its fields, one per group."""
+    hp = (rs_adam_hparams * len(hparams))(*[h if isinstance(h, rs_adam_hparams)
+                                            else rs_adam_hparams(**h) for h in hparams])
+    _check(lib().rs_adamw_step(adamw, hp, len(hparams), _dev(grad_scale), _stream(stream)))
+
+
+def rs_adamw_moments(adamw: int, m, v, dtype: int = RS_F32, stream=None) -> None:
+    """m, v (either may be None): every tensor's moments as `dtype` values,
+    one tensor behind the other."""
+    _check(lib().rs_adamw_moments(adamw, _dev(m), _dev(v), dtype, _stream(stream)))
+
+
 def rs_last_error() -> str:
     return lib().rs_last_error().decode()
 
@@ -570,6 +653,69 @@ class Muon:
             rs_muon_free(self.h)
             self.h = None
         self.workspace = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+class AdamW:
+    """Owns one rs_adamw handle (AdamW over tensors outside a plan's buffers),
+    after upload its device workspace, and what is bound to it."""
+
+    def __init__(self, tensors: Sequence):
+        self.h = rs_adamw_plan(tensors)
+        self.tensors = [tuple(t) for t in tensors]
+        self.workspace = None
+        self.arrays = None
+
+    def upload(self, device="cuda", stream=None):
+        import torch
+        nbytes = rs_adamw_device_bytes(self.h)
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        rs_adamw_upload(self.h, self.workspace, nbytes, stream)
+        return self
+
+    def bind(self, params, grads, m, v, amax_m=None, amax_v=None, bf16_out=None, stream=None):
+        """Tensors are checked against the plan's sizes and types."""
+        n = len(self.tensors)
+        lists = [params, grads, m, v, amax_m, amax_v, bf16_out]
+        if any(x is not None and len(x) != n for x in lists):
+            raise RaggedShardError(RS_EINVAL, f"{n} entries per list needed")
+        sizes = {RS_F32: 4, RS_BF16: 2}
+        for i, (numel, p, g, state, block, _) in enumerate(self.tensors):
+            eight = state == RS_STATE_INT8
+            blocks = -(-numel // block) if eight else 0
+            each = ((params, numel, sizes[p]), (grads, numel, sizes[g]), (m, numel, 1 if eight else 4),
+                    (v, numel, 1 if eight else 4), (amax_m, blocks, 4), (amax_v, blocks, 4),
+                    (bf16_out, numel, 2))
+            for x, count, size in each:
+                x = None if x is None else x[i]
+                if x is None or isinstance(x, int) or (count == 0 and x is not params[i]):
+                    continue
+                if x.numel() != count or x.element_size() != size or not x.is_contiguous():
+                    raise RaggedShardError(RS_EINVAL, f"tensor {i}: not {count} contiguous elements "
+                                                      f"of {size} bytes")
+        rs_adamw_bind(self.h, *lists, stream=stream)
+        self.arrays = lists
+        return self
+
+    def l2norm_clip(self, max_norm: float, sumsq, scale=None, stream=None):
+        rs_adamw_l2norm_clip(self.h, max_norm, sumsq, scale, stream)
+
+    def step(self, hparams, grad_scale=None, stream=None):
+        rs_adamw_step(self.h, hparams, grad_scale, stream)
+
+    def moments(self, m, v, dtype: int = RS_F32, stream=None):
+        rs_adamw_moments(self.h, m, v, dtype, stream)
+
+    def free(self):
+        if self.h:
+            rs_adamw_free(self.h)
+            self.h = None
+        self.workspace = self.arrays = None
 
     def __del__(self):
         try:
