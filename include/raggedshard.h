@@ -685,6 +685,82 @@ rs_status rs_router_balance(const void* d_logits, int32_t dtype, int64_t rows, i
                             int32_t* d_counts, float* d_mean_prob, float* d_stats, void* d_work,
                             size_t bytes, void* stream);
 
+/* ------------------------------------------------- tokens to experts and back
+ * What a mixture-of-experts layer does around its experts' products: the
+ * tokens of a router's choices (d_topk of rs_router_balance) brought together
+ * by expert, the experts' rows brought back with the choices' weights, and the
+ * gradients of both.  A choice (t, j), j < k, is taken if d_mask[t] != 0 (NULL:
+ * all rows) and its id lies in [0, experts); an id given twice is taken twice.
+ * Taken choices fill slots expert by expert, in the order of t and then j; an
+ * expert's segment starts at a multiple of `align` slots (1, or the row tile
+ * of the experts' products) and the rest of its last tile is padding.
+ * Rows are `hidden` values at row strides in elements, dtype RS_F32 or
+ * RS_BF16; what lies behind a row's values is not touched.  All arrays need
+ * the alignment of their elements only.  No output shares a byte with another
+ * array but where it says so (RS_EINVAL).  A slot outside [0, slots) counts as
+ * not taken, whatever wrote it; equal slots are the caller's fault (which of
+ * their rows is kept is open).  Sums are binary32 in a fixed order, rounded
+ * once to the output: equal calls give equal bits.  The calls only launch
+ * kernels on `stream` (capturable in a HIP graph). */
+
+/* The slots that a sort of these sizes fills at most, padding included:
+ * rows k + min(experts, rows k) (align - 1); -1 for sizes it refuses. */
+int64_t rs_expert_slots(int64_t rows, int32_t experts, int32_t k, int32_t align);
+
+/* Scratch bytes of rs_expert_sort (they serve every smaller size); 0 for
+ * sizes it refuses. */
+size_t rs_expert_sort_bytes(int64_t rows, int32_t experts, int32_t k);
+
+/* d_start[e], e = 0..experts: first slot of expert e's segment, and the end;
+ * d_count[e]: choices taken of e; d_slot[t k + j]: the choice's slot, -1 if it
+ * is not taken.  d_topk: k ids a row, row stride ldk.  d_work: device scratch,
+ * 16-byte aligned, nothing carried from call to call.
+ * Errors: RS_EINVAL (NULL or misaligned pointer, experts outside 1..1024, k
+ * outside 1..experts, ldk < k, align outside 1..2^16, overlap), RS_EOVERFLOW
+ * (rows k or the slots beyond 2^31 - 1), RS_ENOMEM (bytes too small), RS_EHIP. */
+rs_status rs_expert_sort(const int64_t* d_topk, int64_t rows, int32_t experts, int32_t k,
+                         int64_t ldk, const uint8_t* d_mask, int32_t align, int64_t* d_start,
+                         int32_t* d_count, int32_t* d_slot, void* d_work, size_t bytes,
+                         void* stream);
+
+/* y[slot of (t, j)] = w x[t] for every choice taken, w = d_weight[t ldw + j]
+ * (NULL: 1; a copy bit for bit).  d_y has `slots` rows.  With d_start and
+ * d_count of the sort (both NULL: not) the padding rows of the segments are
+ * set to 0, so that products over whole tiles, and sums over them, stay
+ * finite.  Rows behind the last segment are left as they were.
+ * Its gradient is rs_expert_combine of dy (and with weights their gradient
+ * rs_expert_combine_grad's dweight of x and dy, d_dy NULL).
+ * Errors: RS_EINVAL (as rs_expert_sort; hidden outside 1..2^24, a stride below
+ * the row), RS_EOVERFLOW, RS_EHIP. */
+rs_status rs_expert_dispatch(const void* d_x, int32_t dtype, int64_t rows, int64_t hidden,
+                             int64_t ldx, const int32_t* d_slot, int32_t k, const float* d_weight,
+                             int64_t ldw, int32_t experts, const int64_t* d_start,
+                             const int32_t* d_count, void* d_y, int64_t slots, int64_t ldy,
+                             void* stream);
+
+/* out[t] = add[t] + sum_j w y[slot of (t, j)] over the choices taken, j
+ * ascending (d_add NULL: 0; d_weight NULL: 1).  d_out may be d_add with lda =
+ * ldo (in place).  Errors as rs_expert_dispatch. */
+rs_status rs_expert_combine(const void* d_y, int32_t dtype, int64_t slots, int64_t hidden,
+                            int64_t ldy, const int32_t* d_slot, int64_t rows, int32_t k,
+                            const float* d_weight, int64_t ldw, const void* d_add, int64_t lda,
+                            void* d_out, int64_t ldo, void* stream);
+
+/* Gradients of rs_expert_combine from dout = dloss / dout:
+ *   dy[slot of (t, j)] = w dout[t]          (d_dy NULL: not computed),
+ *   dweight[t lddw + j] = sum_i dout[t][i] y[slot of (t, j)][i], 0 for a
+ *   choice that is not taken.
+ * d_dy may be d_y with lddy = ldy (in place); its padding rows are set to 0
+ * with d_start and d_count, and rows behind the last segment left, as by
+ * rs_expert_dispatch.  (The gradient of add is dout.)  Errors as
+ * rs_expert_dispatch. */
+rs_status rs_expert_combine_grad(const void* d_dout, int32_t dtype, int64_t rows, int64_t hidden,
+                                 int64_t ldo, const void* d_y, int64_t slots, int64_t ldy,
+                                 const int32_t* d_slot, int32_t k, const float* d_weight,
+                                 int64_t ldw, int32_t experts, const int64_t* d_start,
+                                 const int32_t* d_count, void* d_dy, int64_t lddy,
+                                 float* d_dweight, int64_t lddw, void* stream);
+
 /* Synchronises the stream and reports a device-side failure of the
  * one-launch split modes: RS_EHIP if a bounded wait for the other chunks of
  * a block gave up since the last check, or if the caller set the status

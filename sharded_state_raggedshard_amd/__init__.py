@@ -47,6 +47,8 @@ EXPORTS = (
     "rs_router_balance_bytes", "rs_router_balance",
     "rs_adamw_plan", "rs_adamw_free", "rs_adamw_device_bytes", "rs_adamw_upload", "rs_adamw_bind",
     "rs_adamw_l2norm_clip", "rs_adamw_step", "rs_adamw_moments",
+    "rs_expert_slots", "rs_expert_sort_bytes", "rs_expert_sort", "rs_expert_dispatch",
+    "rs_expert_combine", "rs_expert_combine_grad",
 )
 
 
@@ -165,6 +167,16 @@ def lib() -> C.CDLL:
         "rs_adamw_l2norm_clip": ([vp, C.c_double, vp, vp, vp], C.c_int),
         "rs_adamw_step": ([vp, C.POINTER(rs_adam_hparams), i32, vp, vp], C.c_int),
         "rs_adamw_moments": ([vp, vp, vp, i32, vp], C.c_int),
+        "rs_expert_slots": ([i64, i32, i32, i32], i64),
+        "rs_expert_sort_bytes": ([i64, i32, i32], C.c_size_t),
+        "rs_expert_sort": ([vp, i64, i32, i32, i64, vp, i32, vp, vp, vp, vp, C.c_size_t, vp],
+                           C.c_int),
+        "rs_expert_dispatch": ([vp, i32, i64, i64, i64, vp, i32, vp, i64, i32, vp, vp, vp, i64, i64,
+                                vp], C.c_int),
+        "rs_expert_combine": ([vp, i32, i64, i64, i64, vp, i64, i32, vp, i64, vp, i64, vp, i64, vp],
+                              C.c_int),
+        "rs_expert_combine_grad": ([vp, i32, i64, i64, i64, vp, i64, i64, vp, i32, vp, i64, i32, vp,
+                                    vp, vp, i64, vp, i64, vp], C.c_int),
         "rs_last_error": ([], C.c_char_p),
         "rs_version": ([], C.c_char_p),
     }
@@ -190,15 +202,22 @@ def _ptr(x) -> Optional[int]:
     return int(x.data_ptr())
 
 
+_current_device = None
+
+
 def _dev(x) -> Optional[int]:
     """_ptr of a tensor that the current device holds: a launch there with
     another one's memory, or the host's, could fault."""
+    global _current_device
     if x is None or isinstance(x, int):
         return x
-    import torch
-    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+    if _current_device is None:
+        import torch
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    device = x.get_device()
+    if device < 0 or device != _current_device():
         raise RaggedShardError(RS_EINVAL, f"a tensor on {x.device}, not on the current device")
-    return int(x.data_ptr())
+    return x.data_ptr()
 
 
 _current_stream = None
@@ -520,6 +539,59 @@ def rs_router_balance(logits, dtype: int, rows: int, experts: int, ld: int, topk
                                    _ptr(mask), _ptr(start), n_seq, C.byref(hp), _ptr(dlogits), ldd,
                                    _ptr(counts), _ptr(mean_prob), _ptr(stats), _ptr(work), nbytes,
                                    _stream(stream)))
+
+
+def rs_expert_slots(rows: int, experts: int, k: int, align: int = 1) -> int:
+    n = lib().rs_expert_slots(rows, experts, k, align)
+    if n < 0:
+        raise RaggedShardError(RS_EINVAL, lib().rs_last_error().decode())
+    return int(n)
+
+
+def rs_expert_sort_bytes(rows: int, experts: int, k: int) -> int:
+    n = lib().rs_expert_sort_bytes(rows, experts, k)
+    if n == 0:
+        raise RaggedShardError(RS_EINVAL, lib().rs_last_error().decode())
+    return int(n)
+
+
+def rs_expert_sort(topk, rows: int, experts: int, k: int, ldk: int, mask, align: int, start, count,
+                   slot, work, nbytes: int, stream=None) -> None:
+    """topk: int64 [rows, k] expert ids (row stride ldk); mask (or None): one
+    byte per row; start: int64 [experts + 1]; count: int32 [experts]; slot:
+    int32 [rows, k]."""
+    _check(lib().rs_expert_sort(_dev(topk), rows, experts, k, ldk, _dev(mask), align, _dev(start),
+                                _dev(count), _dev(slot), _dev(work), nbytes, _stream(stream)))
+
+
+def rs_expert_dispatch(x, dtype: int, rows: int, hidden: int, ldx: int, slot, k: int, weight,
+                       ldw: int, experts: int, start, count, y, slots: int, ldy: int,
+                       stream=None) -> None:
+    """x: [rows, hidden] to its slots' rows of y [slots, hidden]; weight (or
+    None): fp32 [rows, k]; start and count (or both None: padding rows stay)
+    from rs_expert_sort."""
+    _check(lib().rs_expert_dispatch(_dev(x), dtype, rows, hidden, ldx, _dev(slot), k, _dev(weight),
+                                    ldw, experts, _dev(start), _dev(count), _dev(y), slots, ldy,
+                                    _stream(stream)))
+
+
+def rs_expert_combine(y, dtype: int, slots: int, hidden: int, ldy: int, slot, rows: int, k: int,
+                      weight, ldw: int, add, lda: int, out, ldo: int, stream=None) -> None:
+    """out [rows, hidden] = add (or None) + the weighted sum of the slots'
+    rows of y [slots, hidden]; weight (or None): fp32 [rows, k]."""
+    _check(lib().rs_expert_combine(_dev(y), dtype, slots, hidden, ldy, _dev(slot), rows, k,
+                                   _dev(weight), ldw, _dev(add), lda, _dev(out), ldo,
+                                   _stream(stream)))
+
+
+def rs_expert_combine_grad(dout, dtype: int, rows: int, hidden: int, ldo: int, y, slots: int,
+                           ldy: int, slot, k: int, weight, ldw: int, experts: int, start, count, dy,
+                           lddy: int, dweight, lddw: int, stream=None) -> None:
+    """dy (or None): [slots, hidden], may be y; dweight: fp32 [rows, k]."""
+    _check(lib().rs_expert_combine_grad(_dev(dout), dtype, rows, hidden, ldo, _dev(y), slots, ldy,
+                                        _dev(slot), k, _dev(weight), ldw, experts, _dev(start),
+                                        _dev(count), _dev(dy), lddy, _dev(dweight), lddw,
+                                        _stream(stream)))
 
 
 def rs_adamw_plan(tensors: Sequence) -> int:

@@ -1,0 +1,546 @@
+// Tokens to experts and back, for gfx950: a stable counting sort of the
+// router's choices by expert, the copy of tokens to their slots, the weighted
+// sum of the slots back to tokens, and its gradient.
+//
+// The sort moves 12 bytes a choice and is bound by its launches.  The others
+// move rows: a token's row is read once for its k slots (dispatch, gradient)
+// or written once from them (combine), a wave or workgroup to a token, so
+// everything is read once and written once; HBM bounds them.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "experts.hpp"
+#include "lanes.hpp"
+#include "row_common.hpp"
+
+namespace rs {
+namespace {
+
+using namespace rows;
+
+// ------------------------------------------------------------------- sort
+
+// Expert of choice i, `experts` for one that is not taken.
+__device__ __forceinline__ int choice(const ExpertSort& a, uint32_t i) {
+    const uint32_t t = i / (uint32_t)a.k, j = i - t * (uint32_t)a.k;
+    if (a.mask && a.mask[t] == 0) return a.experts;
+    const int64_t id = a.topk[(int64_t)t * a.ldk + j];
+    return id >= 0 && id < a.experts ? (int)id : a.experts;
+}
+
+__device__ __forceinline__ int lds_load(const int* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+__device__ __forceinline__ void lds_store(int* p, int v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+
+// Choices [c0, c1) counted per expert by one wave (hist: LDS, may be shared).
+__device__ __forceinline__ void count_choices(const ExpertSort& a, int64_t c0, int64_t c1, int* hist) {
+    for (int64_t i = c0 + lanes::lane(); i < c1; i += 64) {
+        const int id = choice(a, (uint32_t)i);
+        if (id < a.experts) atomicAdd(&hist[id], 1);
+    }
+}
+
+// Slots of choices [c0, c1) by one wave, in order: the next of expert e is
+// first[e] + next[e].  Lanes of one expert find each other by the bits of its
+// id, and the lowest of them moves next[e] on; a wave's LDS accesses take
+// effect in its order.
+__device__ __forceinline__ void place_choices(const ExpertSort& a, int64_t c0, int64_t c1, const int* first,
+                                              int* next) {
+    const int bits = 32 - __builtin_clz((unsigned)a.experts);
+    for (int64_t i0 = c0; i0 < c1; i0 += 64) {
+        const int64_t i = i0 + lanes::lane();
+        const int id = i < c1 ? choice(a, (uint32_t)i) : a.experts;
+        uint64_t same = ~uint64_t(0);
+        for (int b = 0; b < bits; ++b) {
+            const bool one = (id >> b) & 1;
+            const uint64_t have = __ballot(one);
+            same &= one ? have : ~have;
+        }
+        const int rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
+        int slot = -1;
+        if (id < a.experts) {
+            const int at = lds_load(&next[id]);
+            slot = first[id] + at + rank;
+            if (rank == 0) lds_store(&next[id], at + __popcll(same));
+        }
+        if (i < c1) a.slot[i] = slot;
+    }
+}
+
+// counts[0 .. experts) to first slots, by one wave; `write`: to d_start too.
+__device__ __forceinline__ void first_slots(const ExpertSort& a, int* counts, bool write) {
+    const int lane = lanes::lane(), per = (a.experts + 63) / 64;
+    const int e0 = lane * per;
+    int sum = 0;
+    for (int e = e0; e < e0 + per && e < a.experts; ++e) sum += (counts[e] + a.align - 1) / a.align * a.align;
+    int before = sum;
+    for (int off = 1; off < 64; off <<= 1) {
+        const int x = __shfl_up(before, off, 64);
+        if (lane >= off) before += x;
+    }
+    before -= sum;
+    for (int e = e0; e < e0 + per && e < a.experts; ++e) {
+        const int c = (counts[e] + a.align - 1) / a.align * a.align;
+        counts[e] = before;
+        if (write) a.start[e] = before;
+        before += c;
+        if (write && e == a.experts - 1) a.start[a.experts] = before;
+    }
+}
+
+// All choices in one workgroup of WAVES waves.
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void sort_small_kernel(ExpertSort a) {
+    extern __shared__ int lds[];
+    constexpr int NT = 64 * WAVES;
+    const int tid = threadIdx.x, wave = lanes::wave(), E = a.experts;
+    int* hist = lds;          // per wave
+    int* first = lds + WAVES * E;
+    for (int i = tid; i < WAVES * E; i += NT) hist[i] = 0;
+    __syncthreads();
+    const int64_t n = a.rows * a.k, per = (n + NT - 1) / NT * 64;
+    const int64_t c0 = min(n, wave * per), c1 = min(n, c0 + per);
+    count_choices(a, c0, c1, hist + wave * E);
+    __syncthreads();
+    for (int e = tid; e < E; e += NT) {
+        int sum = 0;
+        for (int w = 0; w < WAVES; ++w) {
+            const int c = hist[w * E + e];
+            hist[w * E + e] = sum;
+            sum += c;
+        }
+        first[e] = sum;
+        a.count[e] = sum;
+    }
+    __syncthreads();
+    if (wave == 0) first_slots(a, first, true);
+    __syncthreads();
+    place_choices(a, c0, c1, first, hist + wave * E);
+}
+
+// Many choices, first of three launches: chunk c counts its choices.
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(ExpertSort a, int64_t chunk) {
+    extern __shared__ int hist[];
+    const int tid = threadIdx.x, E = a.experts;
+    for (int e = tid; e < E; e += kSortThreads) hist[e] = 0;
+    __syncthreads();
+    const int64_t n = a.rows * a.k, c0 = blockIdx.x * chunk, c1 = min(n, c0 + chunk);
+    const int64_t per = chunk / (kSortThreads / 64), w0 = c0 + lanes::wave() * per;
+    count_choices(a, min(w0, c1), min(w0 + per, c1), hist);
+    __syncthreads();
+    for (int e = tid; e < E; e += kSortThreads) a.part[(int64_t)blockIdx.x * E + e] = hist[e];
+}
+
+// Second: an expert's counts to what the chunks before hold, a lane an expert
+// and a wave a sixteenth of the chunks.
+constexpr int kScanWaves = 16;
+__global__ __launch_bounds__(64 * kScanWaves) void sort_scan_kernel(ExpertSort a, int chunks) {
+    __shared__ int sums[kScanWaves][64];
+    const int lane = lanes::lane(), wave = lanes::wave(), E = a.experts;
+    const int e = blockIdx.x * 64 + lane;
+    const int per = (chunks + kScanWaves - 1) / kScanWaves;
+    const int c0 = min(chunks, wave * per), c1 = min(chunks, c0 + per);
+    int sum = 0;
+    if (e < E)
+        for (int c = c0; c < c1; ++c) sum += a.part[(int64_t)c * E + e];
+    sums[wave][lane] = sum;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < kScanWaves; ++w) {
+        if (w == wave) before = all;
+        all += sums[w][lane];
+    }
+    if (e >= E) return;
+    for (int c = c0; c < c1; ++c) {
+        const int x = a.part[(int64_t)c * E + e];
+        a.part[(int64_t)c * E + e] = before;
+        before += x;
+    }
+    if (wave == 0) a.count[e] = all;
+}
+
+// Third: the slots.
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(ExpertSort a, int64_t chunk) {
+    constexpr int WAVES = kSortThreads / 64;
+    extern __shared__ int lds[];
+    const int tid = threadIdx.x, wave = lanes::wave(), E = a.experts;
+    int* hist = lds;
+    int* first = lds + WAVES * E;
+    for (int i = tid; i < WAVES * E; i += kSortThreads) hist[i] = 0;
+    for (int e = tid; e < E; e += kSortThreads) first[e] = a.count[e];
+    __syncthreads();
+    const int64_t n = a.rows * a.k, b0 = blockIdx.x * chunk, b1 = min(n, b0 + chunk);
+    const int64_t per = chunk / WAVES;
+    const int64_t c0 = min(b0 + wave * per, b1), c1 = min(c0 + per, b1);
+    count_choices(a, c0, c1, hist + wave * E);
+    if (wave == 0) first_slots(a, first, blockIdx.x == 0);
+    __syncthreads();
+    for (int e = tid; e < E; e += kSortThreads) {
+        int sum = a.part[(int64_t)blockIdx.x * E + e];
+        for (int w = 0; w < WAVES; ++w) {
+            const int c = hist[w * E + e];
+            hist[w * E + e] = sum;
+            sum += c;
+        }
+    }
+    __syncthreads();
+    place_choices(a, c0, c1, first, hist + wave * E);
+}
+
+// -------------------------------------------------------------------- rows
+
+// A row of `hidden` values in 16-byte pieces and a tail of single values.
+// Rows of an odd length start at any element, on either side of a copy.
+template <typename T>
+struct RowShape {
+    static constexpr int N = Vec<T>::n;
+    int pieces, tail;
+    __device__ __forceinline__ explicit RowShape(int64_t hidden)
+        : pieces((int)(hidden / N)), tail((int)(hidden % N)) {}
+};
+
+// The padding rows of every expert's segment to 0, spread over all waves of
+// the launch (`wave` of `waves`): a wave takes every parts-th padding row of
+// an expert.
+template <typename T>
+__device__ __forceinline__ void zero_padding(const ExpertRows& a, T* y, int64_t ldy, int64_t wave, int64_t waves) {
+    const RowShape<T> shape(a.hidden);
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    const int lane = lanes::lane();
+    const int64_t parts = max(int64_t(1), min(int64_t(64), waves / a.experts));
+    for (int64_t q = wave; q < parts * a.experts; q += waves) {
+        const int64_t e = q / parts, used = max(int64_t(0), a.start[e]) + max(0, a.count[e]);
+        const int64_t end = min(a.start[e + 1], a.slots);
+        for (int64_t r = used + (q - e * parts); r < end; r += parts) {
+            T* to = y + r * ldy;
+            for (int p = lane; p < shape.pieces; p += 64) store16(to + p * shape.N, zero);
+            if (lane < shape.tail) to[shape.pieces * shape.N + lane] = T(0);
+        }
+    }
+}
+
+// A wave's share of a row: pieces [p0, p1), at most 64 U of them; the last
+// share has the tail.
+struct Share {
+    int p0, p1;
+    bool last;
+};
+template <int U>
+__host__ __device__ __forceinline__ int shares_of(int pieces) {
+    return pieces <= 64 * U ? 1 : (pieces + 64 * U - 1) / (64 * U);
+}
+__device__ __forceinline__ Share share_of(int pieces, int shares, int i) {
+    const int per = (pieces + shares - 1) / shares;
+    const int p0 = i * per;
+    return Share{p0 < pieces ? p0 : pieces, p0 + per < pieces ? p0 + per : pieces, i == shares - 1};
+}
+
+constexpr int kRowThreads = 256;
+
+// A wave takes a share of a token's row and writes it to its k slots.
+constexpr int kDispatchPieces = 4;
+template <typename T, bool WEIGHTED>
+__global__ __launch_bounds__(kRowThreads) void dispatch_kernel(ExpertRows a, const T* x, int64_t ldx, T* y, int64_t ldy,
+                                                               int shares) {
+    constexpr int N = Vec<T>::n, U = kDispatchPieces, WAVES = kRowThreads / 64;
+    const RowShape<T> shape(a.hidden);
+    const int lane = lanes::lane();
+    const int64_t items = a.rows * shares, wave0 = blockIdx.x * (int64_t)WAVES + lanes::wave();
+    const int64_t waves = gridDim.x * (int64_t)WAVES;
+    for (int64_t item = wave0; item < items; item += waves) {
+        const int64_t t = item / shares;
+        const Share sh = share_of(shape.pieces, shares, (int)(item - t * shares));
+        const T* from = x + t * ldx;
+        u32x4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int p = sh.p0 + u * 64 + lane;
+            if (p < sh.p1) v[u] = load16(from + p * N);
+        }
+        const bool tail = sh.last && lane < shape.tail;
+        const int tail_at = shape.pieces * N + lane;
+        const T one = tail ? from[tail_at] : T(0);
+        const int32_t* slot = a.slot + t * a.k;
+        for (int j = 0; j < a.k; ++j) {
+            const int s = slot[j];
+            if (s < 0 || s >= a.slots) continue;
+            T* to = y + s * ldy;
+            const float w = WEIGHTED ? a.weight[t * a.ldw + j] : 1.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int p = sh.p0 + u * 64 + lane;
+                if (p >= sh.p1) continue;
+                if (WEIGHTED) {
+                    float f[N];
+                    Vec<T>::open(v[u], f);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) f[i] *= w;
+                    store16(to + p * N, Vec<T>::close(f));
+                } else {
+                    store16(to + p * N, v[u]);
+                }
+            }
+            if (tail) to[tail_at] = WEIGHTED ? Vec<T>::pack(Vec<T>::one(one) * w) : one;
+        }
+    }
+    if (a.start) zero_padding(a, y, ldy, wave0, waves);
+}
+
+// A wave takes a share of a token's row from its k slots, B of them in flight.
+// Sums are binary32, in the order of the choices.
+constexpr int kCombinePieces = 2;
+template <typename T>
+__global__ __launch_bounds__(kRowThreads) void combine_kernel(ExpertRows a, const T* y, int64_t ldy, const T* add,
+                                                              int64_t lda, T* out, int64_t ldo, int shares) {
+    constexpr int N = Vec<T>::n, U = kCombinePieces, B = 4, WAVES = kRowThreads / 64;
+    const RowShape<T> shape(a.hidden);
+    const int lane = lanes::lane();
+    const int64_t items = a.rows * shares;
+    for (int64_t item = blockIdx.x * (int64_t)WAVES + lanes::wave(); item < items; item += gridDim.x * (int64_t)WAVES) {
+        const int64_t t = item / shares;
+        const Share sh = share_of(shape.pieces, shares, (int)(item - t * shares));
+        const bool tail = sh.last && lane < shape.tail;
+        const int tail_at = shape.pieces * N + lane;
+        const int32_t* slot = a.slot + t * a.k;
+        float acc[U][N] = {}, acc_tail = 0.0f;
+        if (add) {
+            const T* from = add + t * lda;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int p = sh.p0 + u * 64 + lane;
+                if (p < sh.p1) Vec<T>::open(load16(from + p * N), acc[u]);
+            }
+            if (tail) acc_tail = Vec<T>::one(from[tail_at]);
+        }
+        for (int j0 = 0; j0 < a.k; j0 += B) {
+            u32x4 v[B][U];
+            T one[B];
+            float w[B];
+            bool has[B];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int j = j0 + b, s = j < a.k ? slot[j] : -1;
+                has[b] = s >= 0 && s < a.slots;
+                if (!has[b]) continue;
+                w[b] = a.weight ? a.weight[t * a.ldw + j] : 1.0f;
+                const T* from = y + s * ldy;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int p = sh.p0 + u * 64 + lane;
+                    if (p < sh.p1) v[b][u] = load16_once(from + p * N);
+                }
+                if (tail) one[b] = from[tail_at];
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                if (!has[b]) continue;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float f[N];
+                    Vec<T>::open(v[b][u], f);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[u][i] = __builtin_fmaf(w[b], f[i], acc[u][i]);
+                }
+                if (tail) acc_tail = __builtin_fmaf(w[b], Vec<T>::one(one[b]), acc_tail);
+            }
+        }
+        T* to = out + t * ldo;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int p = sh.p0 + u * 64 + lane;
+            if (p < sh.p1) store16(to + p * N, Vec<T>::close(acc[u]));
+        }
+        if (tail) to[tail_at] = Vec<T>::pack(acc_tail);
+    }
+}
+
+// A workgroup takes a token: its gradient row stays in registers while the k
+// slots' rows pass, each giving one dot product and taking w dout.  Rows
+// longer than U NT pieces go in several turns.  A dot product is a lane's
+// binary32 chain of up to U N products a turn, then the lanes' in a fixed
+// order.
+constexpr int kGradPieces = 4;
+template <typename T, int NT>
+__global__ __launch_bounds__(NT) void combine_grad_kernel(ExpertRows a, const T* dout, int64_t ldo, const T* y,
+                                                          int64_t ldy, T* dy, int64_t lddy, float* dweight,
+                                                          int64_t lddw) {
+    constexpr int N = Vec<T>::n, U = kGradPieces, WAVES = NT / 64, B = 2;
+    extern __shared__ float red[];  // WAVES x k
+    const RowShape<T> shape(a.hidden);
+    const int tid = threadIdx.x, wave = lanes::wave();
+    for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
+        const T* from = dout + t * ldo;
+        const int32_t* slot = a.slot + t * a.k;
+        const int turns = shape.pieces > 0 ? (shape.pieces + U * NT - 1) / (U * NT) : 1;
+        for (int turn = 0; turn < turns; ++turn) {
+            const int p0 = turn * U * NT + tid;
+            u32x4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                v[u] = u32x4{0u, 0u, 0u, 0u};
+                if (p0 + u * NT < shape.pieces) v[u] = load16(from + (p0 + u * NT) * N);
+            }
+            const bool tail = turn == turns - 1 && tid < shape.tail;
+            const int tail_at = shape.pieces * N + tid;
+            const float vt = tail ? Vec<T>::one(from[tail_at]) : 0.0f;
+            for (int j0 = 0; j0 < a.k; j0 += B) {
+                u32x4 q[B][U];
+                float qt[B];
+                int at[B];
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    const int j = j0 + b, s = j < a.k ? slot[j] : -1;
+                    at[b] = s < a.slots ? s : -1;
+                    qt[b] = 0.0f;
+                    if (at[b] < 0) continue;
+                    const T* row = y + at[b] * ldy;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        q[b][u] = u32x4{0u, 0u, 0u, 0u};
+                        if (p0 + u * NT < shape.pieces) q[b][u] = load16_once(row + (p0 + u * NT) * N);
+                    }
+                    if (tail) qt[b] = Vec<T>::one(row[tail_at]);
+                }
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    const int j = j0 + b;
+                    if (j >= a.k) break;
+                    float dot = 0.0f;
+                    if (at[b] >= 0) {
+                        const float w = a.weight ? a.weight[t * a.ldw + j] : 1.0f;
+                        T* to = dy + at[b] * lddy;
+                        float lo = 0.0f, hi = vt * qt[b];
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            float f[N], g[N];
+                            Vec<T>::open(v[u], f);
+                            Vec<T>::open(q[b][u], g);
+#pragma unroll
+                            for (int i = 0; i < N; i += 2) {
+                                lo = __builtin_fmaf(f[i], g[i], lo);
+                                hi = __builtin_fmaf(f[i + 1], g[i + 1], hi);
+                            }
+                            if (dy && p0 + u * NT < shape.pieces) {
+#pragma unroll
+                                for (int i = 0; i < N; ++i) f[i] *= w;
+                                store16(to + (p0 + u * NT) * N, Vec<T>::close(f));
+                            }
+                        }
+                        if (dy && tail) to[tail_at] = Vec<T>::pack(vt * w);
+                        dot = lanes::sum<64>(lo + hi);
+                    }
+                    if (lanes::lane() == 0) red[wave * a.k + j] = turn == 0 ? dot : red[wave * a.k + j] + dot;
+                }
+            }
+        }
+        __syncthreads();
+        for (int j = tid; j < a.k; j += NT) {
+            float sum = red[j];
+            for (int w = 1; w < WAVES; ++w) sum += red[w * a.k + j];
+            dweight[t * lddw + j] = sum;
+        }
+        __syncthreads();
+    }
+    if (a.start && dy) zero_padding(a, dy, lddy, blockIdx.x * (int64_t)WAVES + wave, gridDim.x * (int64_t)WAVES);
+}
+
+// Workgroups of a launch over `items` waves' work; enough of them to clear
+// the experts' padding too.
+unsigned row_grid(const ExpertRows& a, int64_t items, int waves, bool padding) {
+    int64_t n = (items + waves - 1) / waves;
+    if (padding) n = std::max<int64_t>(n, a.experts);
+    return grid_of(n);
+}
+
+template <typename T>
+hipError_t dispatch(const ExpertRows& a, const void* x, int64_t ldx, void* y, int64_t ldy, hipStream_t s) {
+    const int shares = shares_of<kDispatchPieces>((int)(a.hidden / Vec<T>::n));
+    const unsigned g = row_grid(a, a.rows * shares, kRowThreads / 64, a.start);
+    if (g == 0) return hipSuccess;
+    if (a.weight)
+        hipLaunchKernelGGL((dispatch_kernel<T, true>), dim3(g), dim3(kRowThreads), 0, s, a, static_cast<const T*>(x), ldx,
+                           static_cast<T*>(y), ldy, shares);
+    else
+        hipLaunchKernelGGL((dispatch_kernel<T, false>), dim3(g), dim3(kRowThreads), 0, s, a, static_cast<const T*>(x), ldx,
+                           static_cast<T*>(y), ldy, shares);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t combine(const ExpertRows& a, const void* y, int64_t ldy, const void* add, int64_t lda, void* out,
+                   int64_t ldo, hipStream_t s) {
+    const int shares = shares_of<kCombinePieces>((int)(a.hidden / Vec<T>::n));
+    const unsigned g = row_grid(a, a.rows * shares, kRowThreads / 64, false);
+    if (g == 0) return hipSuccess;
+    hipLaunchKernelGGL(combine_kernel<T>, dim3(g), dim3(kRowThreads), 0, s, a, static_cast<const T*>(y), ldy,
+                       static_cast<const T*>(add), lda, static_cast<T*>(out), ldo, shares);
+    return hipGetLastError();
+}
+
+template <typename T, int NT>
+hipError_t combine_grad_nt(const ExpertRows& a, const void* dout, int64_t ldo, const void* y, int64_t ldy, void* dy,
+                           int64_t lddy, float* dweight, int64_t lddw, hipStream_t s) {
+    const unsigned g = row_grid(a, a.rows, 1, a.start && dy);
+    if (g == 0) return hipSuccess;
+    const size_t lds = size_t(NT / 64) * size_t(a.k) * sizeof(float);
+    hipLaunchKernelGGL((combine_grad_kernel<T, NT>), dim3(g), dim3(NT), lds, s, a, static_cast<const T*>(dout), ldo,
+                       static_cast<const T*>(y), ldy, static_cast<T*>(dy), lddy, dweight, lddw);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t combine_grad(const ExpertRows& a, const void* dout, int64_t ldo, const void* y, int64_t ldy, void* dy,
+                        int64_t lddy, float* dweight, int64_t lddw, hipStream_t s) {
+    const int64_t pieces = a.hidden / Vec<T>::n;
+    if (pieces <= 64 * kGradPieces) return combine_grad_nt<T, 64>(a, dout, ldo, y, ldy, dy, lddy, dweight, lddw, s);
+    if (pieces <= 128 * kGradPieces) return combine_grad_nt<T, 128>(a, dout, ldo, y, ldy, dy, lddy, dweight, lddw, s);
+    return combine_grad_nt<T, 256>(a, dout, ldo, y, ldy, dy, lddy, dweight, lddw, s);
+}
+
+}  // namespace
+
+hipError_t launch_expert_sort(const ExpertSort& a, hipStream_t s) {
+    const int64_t n = a.rows * a.k;
+    const size_t row = size_t(a.experts) * sizeof(int);
+    constexpr int64_t kSmall = 8192;
+    if (n <= kSmall) {
+        if (a.experts <= 512)
+            hipLaunchKernelGGL(sort_small_kernel<16>, dim3(1), dim3(1024), 17 * row, s, a);
+        else
+            hipLaunchKernelGGL(sort_small_kernel<8>, dim3(1), dim3(512), 9 * row, s, a);
+        return hipGetLastError();
+    }
+    const int64_t chunk = sort_chunk(n);
+    const int chunks = (int)((n + chunk - 1) / chunk);
+    hipLaunchKernelGGL(sort_count_kernel, dim3(chunks), dim3(kSortThreads), row, s, a, chunk);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(sort_scan_kernel, dim3((a.experts + 63) / 64), dim3(64 * kScanWaves), 0, s, a, chunks);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(sort_place_kernel, dim3(chunks), dim3(kSortThreads), (kSortThreads / 64 + 1) * row, s, a, chunk);
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_dispatch(const ExpertRows& a, const void* x, int64_t ldx, void* y, int64_t ldy,
+                                  hipStream_t s) {
+    return a.f32 ? dispatch<float>(a, x, ldx, y, ldy, s) : dispatch<uint16_t>(a, x, ldx, y, ldy, s);
+}
+
+hipError_t launch_expert_combine(const ExpertRows& a, const void* y, int64_t ldy, const void* add, int64_t lda,
+                                 void* out, int64_t ldo, hipStream_t s) {
+    return a.f32 ? combine<float>(a, y, ldy, add, lda, out, ldo, s)
+                 : combine<uint16_t>(a, y, ldy, add, lda, out, ldo, s);
+}
+
+hipError_t launch_expert_combine_grad(const ExpertRows& a, const void* dout, int64_t ldo, const void* y, int64_t ldy,
+                                      void* dy, int64_t lddy, float* dweight, int64_t lddw, hipStream_t s) {
+    return a.f32 ? combine_grad<float>(a, dout, ldo, y, ldy, dy, lddy, dweight, lddw, s)
+                 : combine_grad<uint16_t>(a, dout, ldo, y, ldy, dy, lddy, dweight, lddw, s);
+}
+
+}  // namespace rs

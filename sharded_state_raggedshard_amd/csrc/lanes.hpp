@@ -1,0 +1,49 @@
+// Device helpers over the lanes of a wave, without LDS: a shuffle through it
+// takes about 100 cycles, a move inside the vector unit a few.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace rs {
+namespace lanes {
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+// f over groups of L neighbouring lanes (f commutes and associates), in every
+// lane and in a fixed order.
+template <int L, typename F>
+__device__ __forceinline__ float reduce(float v, F f) {
+    if (L > 1) v = f(v, dpp<0xB1>(v));   // quad_perm: lane ^ 1
+    if (L > 2) v = f(v, dpp<0x4E>(v));   // quad_perm: lane ^ 2
+    if (L > 4) v = f(v, dpp<0x141>(v));  // mirrored halves of 8 (quads are even by now)
+    if (L > 8) v = f(v, dpp<0x140>(v));  // mirrored rows of 16
+    if (L > 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+    if (L > 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    }
+    return v;
+}
+
+template <int L>
+__device__ __forceinline__ float sum(float v) {
+    return reduce<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ float max(float v) {
+    return reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// Index of the wave in its workgroup, known to be the same in all lanes.
+__device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
+__device__ __forceinline__ int lane() { return (int)(threadIdx.x & 63); }
+
+}  // namespace lanes
+}  // namespace rs
