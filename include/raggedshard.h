@@ -685,6 +685,50 @@ rs_status rs_router_balance(const void* d_logits, int32_t dtype, int64_t rows, i
                             int32_t* d_counts, float* d_mean_prob, float* d_stats, void* d_work,
                             size_t bytes, void* stream);
 
+/* ------------------------------------------------------- token statistics
+ * Of every row of logits, in one pass over them: the log-probability of its
+ * token, the entropy of its distribution, and its most probable alternatives
+ * -- what a sampler reports, and what a loss of the caller's own is made of --
+ * and the logits' gradient from the gradients of the first two.  Rows, strides,
+ * dtypes, tokens and rows that take no part as at the training objectives.
+ * Exponents take log2(e) / temperature rounded to binary32 (a temperature off
+ * by up to 2^-24 of itself); exponentials are binary32, sums as there. */
+
+/* Scratch bytes of rs_token_stats (they serve every smaller size); 0 for sizes
+ * it refuses. */
+size_t rs_token_stats_bytes(int64_t rows, int64_t vocab, int32_t top);
+
+/* With p = softmax(z_t / temperature), for every row t:
+ *   d_logp[t]    = log p[d_target[t]],
+ *   d_entropy[t] = -sum_i p_i log p_i  (terms of p_i = 0 are 0),
+ *   d_top_id[t top + r], d_top_logp[t top + r], r < top: the r-th most probable
+ *                  i and log p_i, equal logits by the lower index; where fewer
+ *                  than top have a logit above -inf, -1 and -inf,
+ *   d_saved[4 t ..]: what rs_token_stats_grad takes of the row.
+ * d_logp, d_entropy and d_saved may be NULL; with top = 0 the alternatives too.
+ * d_target NULL: rows have no token and all take part (d_logp NULL).  A row
+ * that takes no part has logp 0, entropy 0 and no alternatives (-1, -inf); one
+ * with a NaN or +inf has NaN, and ids of -1.  Errors: RS_EINVAL (as
+ * rs_token_logp; top outside 0..32, d_logp without d_target, overlap),
+ * RS_EOVERFLOW, RS_ENOMEM, RS_EHIP. */
+rs_status rs_token_stats(const void* d_logits, int32_t dtype, int64_t rows, int64_t vocab,
+                         int64_t ld, const int64_t* d_target, double temperature, float* d_logp,
+                         float* d_entropy, int32_t top, int64_t* d_top_id, float* d_top_logp,
+                         float* d_saved, void* d_work, size_t bytes, void* stream);
+
+/* dloss / dlogits from c = d_dlogp[t] = dloss / dlogp and b = d_dentropy[t] =
+ * dloss / dentropy (either NULL: 0), for the same logits, tokens and
+ * temperature and what rs_token_stats saved of them:
+ *   dz_i = (c ([i = token] - p_i) - b p_i (log p_i + entropy)) / temperature,
+ * as dtype, 0 for a row that takes no part and where c and b are both 0.
+ * d_dlogits may be d_logits with ldd = ld (in place).  Errors: RS_EINVAL (as
+ * rs_policy_loss; d_dlogp without d_target), RS_EOVERFLOW, RS_EHIP. */
+rs_status rs_token_stats_grad(const void* d_logits, int32_t dtype, int64_t rows, int64_t vocab,
+                              int64_t ld, const int64_t* d_target, double temperature,
+                              const float* d_saved, const float* d_dlogp,
+                              const float* d_dentropy, void* d_dlogits, int64_t ldd,
+                              void* stream);
+
 /* ------------------------------------------------- tokens to experts and back
  * What a mixture-of-experts layer does around its experts' products: the
  * tokens of a router's choices (d_topk of rs_router_balance) brought together

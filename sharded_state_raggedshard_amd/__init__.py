@@ -49,6 +49,7 @@ EXPORTS = (
     "rs_adamw_l2norm_clip", "rs_adamw_step", "rs_adamw_moments",
     "rs_expert_slots", "rs_expert_sort_bytes", "rs_expert_sort", "rs_expert_dispatch",
     "rs_expert_combine", "rs_expert_combine_grad",
+    "rs_token_stats_bytes", "rs_token_stats", "rs_token_stats_grad",
 )
 
 
@@ -177,6 +178,11 @@ def lib() -> C.CDLL:
                               C.c_int),
         "rs_expert_combine_grad": ([vp, i32, i64, i64, i64, vp, i64, i64, vp, i32, vp, i64, i32, vp,
                                     vp, vp, i64, vp, i64, vp], C.c_int),
+        "rs_token_stats_bytes": ([i64, i64, i32], C.c_size_t),
+        "rs_token_stats": ([vp, i32, i64, i64, i64, vp, C.c_double, vp, vp, i32, vp, vp, vp, vp,
+                            C.c_size_t, vp], C.c_int),
+        "rs_token_stats_grad": ([vp, i32, i64, i64, i64, vp, C.c_double, vp, vp, vp, vp, i64, vp],
+                                C.c_int),
         "rs_last_error": ([], C.c_char_p),
         "rs_version": ([], C.c_char_p),
     }
@@ -539,6 +545,34 @@ def rs_router_balance(logits, dtype: int, rows: int, experts: int, ld: int, topk
                                    _ptr(mask), _ptr(start), n_seq, C.byref(hp), _ptr(dlogits), ldd,
                                    _ptr(counts), _ptr(mean_prob), _ptr(stats), _ptr(work), nbytes,
                                    _stream(stream)))
+
+
+def rs_token_stats_bytes(rows: int, vocab: int, top: int = 0) -> int:
+    n = lib().rs_token_stats_bytes(rows, vocab, top)
+    if n == 0:
+        raise RaggedShardError(RS_EINVAL, lib().rs_last_error().decode())
+    return int(n)
+
+
+def rs_token_stats(logits, dtype: int, rows: int, vocab: int, ld: int, target, logp, entropy,
+                   top: int, top_id, top_logp, saved, work, nbytes: int,
+                   temperature: float = 1.0, stream=None) -> None:
+    """target (or None): int64 per row; logp, entropy (or None): fp32 per row;
+    top_id: int64, top_logp: fp32 [rows, top] (None with top = 0); saved (or
+    None): fp32 [rows, 4], for rs_token_stats_grad."""
+    _check(lib().rs_token_stats(_dev(logits), dtype, rows, vocab, ld, _dev(target), temperature,
+                                _dev(logp), _dev(entropy), top, _dev(top_id), _dev(top_logp),
+                                _dev(saved), _dev(work), nbytes, _stream(stream)))
+
+
+def rs_token_stats_grad(logits, dtype: int, rows: int, vocab: int, ld: int, target, saved, dlogp,
+                        dentropy, dlogits, ldd: int, temperature: float = 1.0,
+                        stream=None) -> None:
+    """dlogp, dentropy (either may be None): fp32 per row; dlogits: as logits,
+    row stride ldd."""
+    _check(lib().rs_token_stats_grad(_dev(logits), dtype, rows, vocab, ld, _dev(target),
+                                     temperature, _dev(saved), _dev(dlogp), _dev(dentropy),
+                                     _dev(dlogits), ldd, _stream(stream)))
 
 
 def rs_expert_slots(rows: int, experts: int, k: int, align: int = 1) -> int:

@@ -18,7 +18,7 @@ BUILD = os.path.join(PKG, "_build")
 SOURCES = ["plan.cpp", "abi.cpp", "copy_kernels.hip", "adam8_kernels.hip", "fp8_kernels.hip",
            "muon.cpp", "muon_kernels.hip", "objectives.cpp", "objective_kernels.hip",
            "router.cpp", "router_kernels.hip", "adamw.cpp", "adamw_kernels.hip",
-           "experts.cpp", "expert_kernels.hip"]
+           "experts.cpp", "expert_kernels.hip", "token_stats.cpp", "token_stats_kernels.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
