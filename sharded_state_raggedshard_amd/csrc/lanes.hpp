@@ -41,6 +41,33 @@ __device__ __forceinline__ float max(float v) {
     return reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
+// The same sum of binary64 values.
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const int lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, true);
+    const int hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, ((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+}
+__device__ __forceinline__ double sum64(double v) {
+    v += dpp<0xB1>(v);
+    v += dpp<0x4E>(v);
+    v += dpp<0x141>(v);
+    v += dpp<0x140>(v);
+    const auto swap = [](double x, bool far) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, x);
+        const uint32_t lo = (uint32_t)u, hi = (uint32_t)(u >> 32);
+        const auto a = far ? __builtin_amdgcn_permlane32_swap(lo, lo, false, false)
+                           : __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+        const auto b = far ? __builtin_amdgcn_permlane32_swap(hi, hi, false, false)
+                           : __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+        return __builtin_bit_cast(double, ((uint64_t)b[0] << 32) | a[0]) +
+               __builtin_bit_cast(double, ((uint64_t)b[1] << 32) | a[1]);
+    };
+    v = swap(v, false);
+    return swap(v, true);
+}
+
 // Index of the wave in its workgroup, known to be the same in all lanes.
 __device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
 __device__ __forceinline__ int lane() { return (int)(threadIdx.x & 63); }

@@ -28,32 +28,42 @@ constexpr float kLeast = -200.0f;
 
 __device__ __forceinline__ float exponent(float x, float m, float k) { return (x - m) * k; }
 
-// Maximum and sums of a thread's share of a row, a part of it or a row, the
-// row's token in the maximum from the start but not in the sums (it joins
-// last: where it is nearly the whole row, any sum with it would round away
-// the rest that 1 - p and the entropy are made of).  `best` is the share's own
-// largest value.  Sums are binary64; the C values of a call are added up in
+// A value that is the same in all lanes, as one that the compiler knows to be.
+__device__ __forceinline__ float wave_uniform(float v) {
+    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
+}
+
+// Sums of a thread's share of a row, a part of it or a row around a reference
+// that the wave's threads share: the row's token at first (it is in no sum, but
+// joins last: where it is nearly the whole row, any sum with it would round
+// away the rest that 1 - p and the entropy are made of), then any value seen
+// that lies more than a factor 2 above.  A thread's own maximum as a reference
+// cost a rescaling of binary64 sums for every 32 values.  `best` is the share's
+// own largest value.  Sums are binary64; the C values of a call are added up in
 // binary32 in four chains.
 struct Sums {
-    float m, best;
+    float best;
     double s, w;
 
-    __device__ __forceinline__ void rescale(float M, float r, float k) {
-        const float d = fmaxf(exponent(m, r, k), kLeast);
+    __device__ __forceinline__ void rescale(float from, float to, float k) {
+        const float d = fmaxf(exponent(from, to, k), kLeast);
         const double f = (double)exp2_fast(d);
         w = f * __builtin_fma((double)d, s, w);
         s *= f;
-        m = M;
     }
 
     template <int C>
-    __device__ __forceinline__ void take(const float (&x)[C], float k) {
+    __device__ __forceinline__ void take(const float (&x)[C], float& ref, float k) {
         float v = x[0];
 #pragma unroll
         for (int i = 1; i < C; ++i) v = fmaxf(v, x[i]);
         best = fmaxf(best, v);
-        const float M = fmaxf(m, v);
-        const float r = M == kNegInf ? 0.0f : M;  // -inf - 0 gives 2^-inf = 0
+        if (__any(exponent(v, ref, k) > 1.0f)) {
+            const float to = wave_uniform(lanes::max<64>(fmaxf(ref, v)));
+            rescale(ref, to, k);
+            ref = to;
+        }
+        const float r = ref == kNegInf ? 0.0f : ref;  // -inf - 0 gives 2^-inf = 0
         float a[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < C; ++i) {
@@ -61,44 +71,28 @@ struct Sums {
             a[i % 4] += e;
             b[i % 4] = __builtin_fmaf(e, fmaxf(d, kLeast), b[i % 4]);
         }
-        rescale(M, r, k);
         s += (double)((a[0] + a[1]) + (a[2] + a[3]));
         w += (double)((b[0] + b[1]) + (b[2] + b[3]));
     }
-
-    __device__ __forceinline__ void join(float m2, double s2, double w2, float k) {
-        Sums o{m2, kNegInf, s2, w2};
-        const float M = fmaxf(m, m2), r = M == kNegInf ? 0.0f : M;
-        rescale(M, r, k);
-        o.rescale(M, r, k);
-        s += o.s;
-        w += o.w;
-    }
 };
-
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-    return v;
-}
 
 // What the statistics of a row come to, its token among the values.
 struct RowEnd {
-    float m, token;
+    float m, token;     // m: the reference
     bool empty;         // nothing but -inf
     double rest, S;     // sums of e, `rest` without the token's
     double ln_s, down;  // ln S; E[(m - z) / T]
 };
 
-__device__ __forceinline__ RowEnd row_end(const Sums& x, float token, bool has, float k) {
+__device__ __forceinline__ RowEnd row_end(const Sums& x, float ref, float token, bool has, float k) {
     RowEnd e;
-    const float r = x.m == kNegInf ? 0.0f : x.m, d = exponent(token, r, k);
+    const float r = ref == kNegInf ? 0.0f : ref, d = exponent(token, r, k);
     const float own = has ? exp2_fast(d) : 0.0f;
     e.m = r;
     e.token = token;
     e.rest = x.s;
     e.S = x.s + (double)own;
-    e.empty = x.m == kNegInf && e.S == 0.0;
+    e.empty = ref == kNegInf && e.S == 0.0;
     const double w = x.w + (has ? (double)own * (double)fmaxf(d, kLeast) : 0.0);
     // ln(1 + rest) of a small rest: 1 + rest has rounded its digits away
     const bool sure = own == 1.0f && e.rest < 0x1p-20;
@@ -159,17 +153,38 @@ struct Candidates {
 
 __device__ __forceinline__ bool before(float v, int i, float w, int j) { return v > w || (v == w && i < j); }
 
-// The n-th largest of the wave's 64 values (n <= 64), ties counted by lane.
+__device__ __forceinline__ float lane_value(float v, int l) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+
+// The n-th largest of the wave's 64 values (n <= 64): the least of those that
+// fewer than n are above.
 __device__ __forceinline__ float nth_of_wave(float v, int n) {
+    int above = 0;
+#pragma unroll
+    for (int l = 0; l < 64; ++l) above += lane_value(v, l) > v ? 1 : 0;
+    return wave_uniform(-lanes::max<64>(above < n ? -v : kNegInf));
+}
+
+// Ranks of n candidates, and write(rank, value, index) for the best `top` of
+// them, by one wave; write(rank, -inf, -1) for what is missing.
+template <typename F>
+__device__ __forceinline__ void write_best(const float* v, const int32_t* id, int n, int top, F write) {
     const int lane = lanes::lane();
-    int rank = 0;
-#pragma unroll 8
-    for (int l = 0; l < 64; ++l) {
-        const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
-        rank += before(o, l, v, lane) ? 1 : 0;
+    if (n <= 64) {
+        const float mine = lane < n ? v[lane] : kNegInf;
+        const int i = lane < n ? id[lane] : 0x7fffffff;
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += before(lane_value(mine, j), __builtin_amdgcn_readlane(i, j), mine, i) ? 1 : 0;
+        if (lane < n && rank < top) write(rank, mine, i);
+    } else {
+        for (int i = lane; i < n; i += 64) {
+            int rank = 0;
+            for (int j = 0; j < n; ++j) rank += before(v[j], id[j], v[i], id[i]) ? 1 : 0;
+            if (rank < top) write(rank, v[i], id[i]);
+        }
     }
-    const uint64_t at = __ballot(rank == n - 1);
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), __builtin_ctzll(at)));
+    for (int r = n + lane; r < top; r += 64) write(r, kNegInf, -1);
 }
 
 // The values of a part of a row that are taken one by one, a thread each: the
@@ -189,76 +204,105 @@ struct Single {
     __device__ __forceinline__ float value() const { return at < 0 ? kNegInf : Vec<T>::one(raw); }
 };
 
+// A thread's largest value is kept for up to kSegments stretches of its share.
+constexpr int kSegments = 8, kTake = 4;  // kTake pieces a thread in flight
+
 template <int NT>
 struct StatsLds {
-    double s[NT / 64], w[NT / 64];
-    float m[NT / 64];
+    // of the waves; two rows' worth, as a row's end is written by the first
+    // wave while the others go on
+    double s[2][NT / 64], w[2][NT / 64];
+    float ref[2][NT / 64];
     float group[64];
     float least;
-    int32_t hot[NT];
+    float best[kSegments][NT];
+    int32_t hot[kSegments * NT];
     int32_t n_hot;
+    float red[NT / 64];
     Candidates c;
 };
 
-// Sums of the whole workgroup, in a fixed order; valid in every thread.  Ends
-// with a barrier.
+// The stretches of a part: takes of kTake NT pieces, `per` of them each.
 template <int NT>
-__device__ __forceinline__ Sums wg_join(Sums x, float k, StatsLds<NT>& lds) {
-    float M = x.m;
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
-    x.rescale(M, M == kNegInf ? 0.0f : M, k);
-    x.s = wave_sum(x.s);
-    x.w = wave_sum(x.w);
-    if (NT == 64) return x;
-    if (lanes::lane() == 0) {
-        lds.s[threadIdx.x >> 6] = x.s;
-        lds.w[threadIdx.x >> 6] = x.w;
-        lds.m[threadIdx.x >> 6] = M;
+struct Segments {
+    int takes, per, n;
+    __device__ __forceinline__ explicit Segments(const Part& part) {
+        takes = part.v1 > part.v0 ? (part.v1 - part.v0 + kTake * NT - 1) / (kTake * NT) : 0;
+        per = takes > kSegments ? (takes + kSegments - 1) / kSegments : 1;
+        n = (takes + per - 1) / per;
     }
-    __syncthreads();
-    Sums all{lds.m[0], kNegInf, lds.s[0], lds.w[0]};
-#pragma unroll
-    for (int i = 1; i < NT / 64; ++i) all.join(lds.m[i], lds.s[i], lds.w[i], k);
-    __syncthreads();
-    return all;
-}
+};
 
 // The part's best a.top values into lds.c, unordered, from the threads' own
 // largest values.  64 groups of neighbouring threads: the n-th largest of the
 // groups' largest values is reached by n values at least, so the n best are
-// among what reaches it: about n to 2 n values, in the shares of as many
-// threads, which the workgroup reads again.  lds.c.n passes kRoom where that
-// many tie with it or a few shares hold them.
-template <typename T, int NT>
-__device__ __forceinline__ void gather_best(const T* z, const Pieces<T>& ps, const Part& part, int y, float best,
-                                            const Single<T>& one, int n, StatsLds<NT>& lds) {
-    constexpr int N = Vec<T>::n, L = NT / 64;
+// among what reaches it: about n to 2 n values, in as many threads' stretches,
+// which the workgroup reads again (from a cache, if the first read went
+// through it).  lds.c.n passes kRoom where that many tie with it or a few
+// stretches hold them.  Begins behind the barrier that lds.group is written
+// before; ends with one.
+// HELD: a part is one take, still in registers.
+template <typename T, int NT, bool HELD>
+__device__ __forceinline__ void gather_best(const T* z, const Pieces<T>& ps, const Part& part, const Segments<NT>& seg,
+                                            int y, const Single<T>& one, const u32x4 (&held)[kTake], float best,
+                                            int n, StatsLds<NT>& lds) {
+    constexpr int N = Vec<T>::n, B = 4;
     const int tid = threadIdx.x;
-    const float group = lanes::max<L>(best);
-    if (tid % L == 0) lds.group[tid / L] = group;
-    if (tid == 0) lds.n_hot = lds.c.n = 0;
-    __syncthreads();
     if (tid < 64) {
+        if (tid == 0) lds.n_hot = lds.c.n = 0;
         const float least = nth_of_wave(lds.group[tid], n);
         if (tid == 0) lds.least = least;
     }
     __syncthreads();
     const float least = lds.least;
     const auto fits = [&](float x) { return x >= least && x > kNegInf; };
-    if (fits(best)) lds.hot[atomicAdd(&lds.n_hot, 1)] = tid;
     if (one.at >= 0 && fits(one.value())) lds.c.add(one.value(), one.at);
-    __syncthreads();
-    const int hot = lds.n_hot, per = (part.v1 - part.v0 + NT - 1) / NT, yv = ps.piece(y);
-    const T* base = z + ps.head;
-    for (int q = tid; q < hot * per; q += NT) {
-        const int h = q / per, v = part.v0 + lds.hot[h] + (q - h * per) * NT;
-        if (v >= part.v1 || v == yv) continue;
-        float x[N];
-        Vec<T>::open(load16(base + v * N), x);
+    if (HELD) {
+        if (fits(best)) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (fits(x[i])) lds.c.add(x[i], ps.head + v * N + i);
+            for (int u = 0; u < kTake; ++u) {
+                float x[N];
+                Vec<T>::open(held[u], x);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (fits(x[i])) lds.c.add(x[i], ps.head + (part.v0 + tid + u * NT) * N + i);
+            }
+        }
+        __syncthreads();
+        return;
+    }
+    for (int i = 0; i < seg.n; ++i)
+        if (fits(lds.best[i][tid])) lds.hot[atomicAdd(&lds.n_hot, 1)] = i * NT + tid;
+    __syncthreads();
+    // piece j of stretch i of thread h is part.v0 + h + (i length + j) NT;
+    // places are dealt out by a power of two that holds a stretch
+    const int length = seg.per * kTake, shift = length > 1 ? 32 - __builtin_clz((unsigned)(length - 1)) : 0;
+    const int all = lds.n_hot << shift, yv = ps.piece(y);
+    const T* base = z + ps.head;
+    for (int q0 = tid; q0 < all; q0 += B * NT) {
+        u32x4 raw[B];
+        int at[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int q = q0 + b * NT;
+            at[b] = -1;
+            if (q >= all) continue;
+            const int unit = lds.hot[q >> shift], j = q & ((1 << shift) - 1);
+            const int v = part.v0 + unit % NT + ((unit / NT) * length + j) * NT;
+            if (j < length && v < part.v1 && v != yv) at[b] = v;
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (at[b] >= 0) raw[b] = load16(base + at[b] * N);
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (at[b] < 0) continue;
+            float x[N];
+            Vec<T>::open(raw[b], x);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (fits(x[i])) lds.c.add(x[i], ps.head + at[b] * N + i);
+        }
     }
     __syncthreads();
 }
@@ -289,11 +333,11 @@ __device__ void gather_slow(const T* z, const Pieces<T>& ps, const Part& part, i
         }
         if (tid < edges) see(Vec<T>::one(z[ps.edge(tid)]));
         const float most = lanes::max<64>(top);
-        if (lanes::lane() == 0) lds.m[tid >> 6] = most;
+        if (lanes::lane() == 0) lds.red[tid >> 6] = most;
         if (tid == 0) lds.n_hot = 0;
         __syncthreads();
-        last = lds.m[0];
-        for (int i = 1; i < NT / 64; ++i) last = fmaxf(last, lds.m[i]);
+        last = lds.red[0];
+        for (int i = 1; i < NT / 64; ++i) last = fmaxf(last, lds.red[i]);
         if (top == last && count > 0) atomicAdd(&lds.n_hot, count);
         __syncthreads();
         above = found;
@@ -361,20 +405,26 @@ __device__ void gather_slow(const T* z, const Pieces<T>& ps, const Part& part, i
     __syncthreads();
 }
 
-// One workgroup per part of a row.
-template <typename T, int NT, bool TOP>
-__global__ __launch_bounds__(NT) void stats_kernel(TokenStats a) {
-    constexpr int N = Vec<T>::n, U = 4;
+// What stats_kernel does beside the sums: nothing; finds the alternatives; does
+// so in parts of one take.
+enum { TOP_NONE = 0, TOP_LONG = 1, TOP_HELD = 2 };
+
+// One workgroup per part of a row; its first wave ends the row while the
+// others go on to the next.
+template <typename T, int NT, int MODE>
+__global__ __launch_bounds__(NT, MODE == TOP_NONE ? 5 : 4) void stats_kernel(TokenStats a) {
+    constexpr bool TOP = MODE != TOP_NONE;
+    constexpr int N = Vec<T>::n, U = kTake, WAVES = NT / 64;
     __shared__ StatsLds<NT> lds;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = lanes::lane();
     const float k = a.k;
     const int64_t items = a.rows * a.parts;
+    int turn = 0;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int64_t row = a.parts == 1 ? item : item / a.parts;
         const int index = (int)(item - row * a.parts);
-        const bool live = takes_part(a, row);
-        if (!live) {
-            if (a.parts == 1) {
+        if (!takes_part(a, row)) {
+            if (a.parts == 1 && tid < 64) {
                 if (tid == 0) write_row(a, row, false, RowEnd{});
                 if (TOP && tid < a.top) write_top(a, row, tid, 0.0f, -1, RowEnd{});
             }
@@ -385,17 +435,20 @@ __global__ __launch_bounds__(NT) void stats_kernel(TokenStats a) {
         const float token = y >= 0 ? Vec<T>::one(z[y]) : kNegInf;
         const Pieces<T> ps(z, a.vocab);
         const Part part = part_of(z, ps, index, a.parts);
+        const Segments<NT> seg(part);
         const Single<T> one(z, ps, part, y);
         const T* base = z + ps.head;
         const int yv = ps.piece(y);
-        Sums run{token, kNegInf, 0.0, 0.0};
-        for (int v = part.v0 + tid; v < part.v1; v += U * NT) {
-            u32x4 raw[U];
+        Sums run{kNegInf, 0.0, 0.0};
+        float ref = wave_uniform(token), best = kNegInf;
+        u32x4 raw[U] = {};
+        for (int t = 0, next = seg.per, i = 0; t < seg.takes; ++t) {
+            const int v = part.v0 + tid + t * (U * NT);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 raw[u] = Vec<T>::lowest();
                 const int at = v + u * NT;
-                if (at < part.v1 && at != yv) raw[u] = TOP ? load16(base + at * N) : load16_once(base + at * N);
+                if (at < part.v1 && at != yv) raw[u] = load16_once(base + at * N);
             }
             float x[U * N];
 #pragma unroll
@@ -405,49 +458,66 @@ __global__ __launch_bounds__(NT) void stats_kernel(TokenStats a) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) x[u * N + i] = f[i];
             }
-            run.take(x, k);
+            run.take(x, ref, k);
+            if (TOP && (t + 1 == next || t + 1 == seg.takes)) {
+                lds.best[i++][tid] = run.best;
+                best = fmaxf(best, run.best);
+                run.best = kNegInf;
+                next += seg.per;
+            }
         }
-        const float best = run.best;
-        if (tid < 64) run.take({one.at == y ? kNegInf : one.value()}, k);
-        const Sums all = wg_join<NT>(run, k, lds);
-        const RowEnd e = row_end(all, token, y >= 0, k);
-        if (tid == 0) {
-            if (a.parts == 1)
-                write_row(a, row, true, e);
-            else
-                a.stat[item] = PartStat{all.s, all.w, all.m, 0.0f};
+        if (tid < 64) run.take({one.at == y ? kNegInf : one.value()}, ref, k);
+        const double s = lanes::sum64(run.s), w = lanes::sum64(run.w);
+        const int wave = tid >> 6;
+        turn ^= 1;
+        if (lane == 0) {
+            lds.s[turn][wave] = s;
+            lds.w[turn][wave] = w;
+            lds.ref[turn][wave] = ref;
+        }
+        if (TOP) {
+            const float group = lanes::max<WAVES>(best);
+            if (tid % WAVES == 0) lds.group[tid / WAVES] = group;
+        }
+        __syncthreads();
+        if (TOP) {
+            gather_best<T, NT, MODE == TOP_HELD>(z, ps, part, seg, y, one, raw, best, a.top, lds);
+            if (lds.c.n > kRoom) gather_slow<T, NT>(z, ps, part, a.top, lds);
+        }
+        if (tid >= 64) continue;
+        // the waves' sums, a lane each and all of them in every lane
+        const int from = lane % WAVES;
+        Sums all{kNegInf, lds.s[turn][from], lds.w[turn][from]};
+        const float mine = lds.ref[turn][from], top = wave_uniform(lanes::max<64>(mine));
+        all.rescale(mine, top == kNegInf ? 0.0f : top, k);
+#pragma unroll
+        for (int off = 1; off < WAVES; off <<= 1) {
+            all.s += __shfl_xor(all.s, off, 64);
+            all.w += __shfl_xor(all.w, off, 64);
+        }
+        RowEnd e{};
+        if (a.parts == 1) {
+            e = row_end(all, top, token, y >= 0, k);
+            if (tid == 0) write_row(a, row, true, e);
+        } else if (tid == 0) {
+            a.stat[item] = PartStat{all.s, all.w, top, 0.0f};
         }
         if (!TOP) continue;
-        gather_best<T, NT>(z, ps, part, y, best, one, a.top, lds);
-        if (lds.c.n > kRoom) gather_slow<T, NT>(z, ps, part, a.top, lds);
         const int n = lds.c.n;
-        for (int i = tid; i < n; i += NT) {
-            const float v = lds.c.v[i];
-            const int id = lds.c.id[i];
-            int rank = 0;
-            for (int j = 0; j < n; ++j) rank += before(lds.c.v[j], lds.c.id[j], v, id) ? 1 : 0;
-            if (rank >= a.top) continue;
+        const auto write = [&](int rank, float v, int id) {
             if (a.parts == 1) {
                 write_top(a, row, rank, v, id, e);
             } else {
                 a.best[item * a.top + rank] = v;
                 a.best_id[item * a.top + rank] = id;
             }
-        }
-        for (int r = n + tid; r < a.top; r += NT) {
-            if (a.parts == 1) {
-                write_top(a, row, r, kNegInf, -1, e);
-            } else {
-                a.best[item * a.top + r] = kNegInf;
-                a.best_id[item * a.top + r] = -1;
-            }
-        }
-        __syncthreads();
+        };
+        write_best(lds.c.v, lds.c.id, n, a.top, write);
     }
 }
 
 // Rows in several parts: a wave joins a row's statistics, a lane a part, and
-// picks the best of its parts' best, at most 16 a lane.
+// picks the best of its parts' best.
 constexpr int kMostBest = kMaxParts * kMaxTop;
 template <typename T>
 __global__ __launch_bounds__(64) void stats_join_kernel(TokenStats a) {
@@ -463,10 +533,14 @@ __global__ __launch_bounds__(64) void stats_join_kernel(TokenStats a) {
         const int64_t y = a.target ? a.target[row] : -1;
         const float token = y >= 0 ? Vec<T>::one(z[y]) : kNegInf;
         const PartStat p = a.stat[row * a.parts + lane % a.parts];
-        Sums x{p.m, kNegInf, p.s, p.w};
-        for (int off = 1; off < a.parts; off <<= 1)
-            x.join(__shfl_xor(x.m, off, 64), __shfl_xor(x.s, off, 64), __shfl_xor(x.w, off, 64), a.k);
-        e = row_end(x, token, y >= 0, a.k);
+        const float top = wave_uniform(lanes::max<64>(p.m));
+        Sums x{kNegInf, p.s, p.w};
+        x.rescale(p.m, top == kNegInf ? 0.0f : top, a.k);
+        for (int off = 1; off < a.parts; off <<= 1) {
+            x.s += __shfl_xor(x.s, off, 64);
+            x.w += __shfl_xor(x.w, off, 64);
+        }
+        e = row_end(x, top, token, y >= 0, a.k);
     }
     if (lane == 0) write_row(a, row, live, e);
     if (a.top == 0) return;
@@ -474,27 +548,24 @@ __global__ __launch_bounds__(64) void stats_join_kernel(TokenStats a) {
         if (lane < a.top) write_top(a, row, lane, 0.0f, -1, e);
         return;
     }
-    const int n = a.parts * a.top;
-    const float* v = a.best + row * n;
-    const int32_t* id = a.best_id + row * n;
-    float best = kNegInf;
-    for (int i = lane; i < n; i += 64) best = fmaxf(best, v[i]);
-    const float least = nth_of_wave(best, a.top);
+    // 64 / parts lanes a part, the first ones with its largest values: the
+    // n-th largest of the lanes' largest is reached by little more than n
+    const int lanes_each = 64 / a.parts, at0 = lane % lanes_each;
+    const int64_t first = row * a.parts * a.top + (int64_t)(lane / lanes_each) * a.top;
+    const float* v = a.best + first;
+    const int32_t* id = a.best_id + first;
+    const float least = nth_of_wave(at0 < a.top ? v[at0] : kNegInf, a.top);
     if (lane == 0) kept = 0;
     __syncthreads();
-    for (int i = lane; i < n; i += 64) {
-        if (!(v[i] >= least) || v[i] == kNegInf) continue;
+    for (int i = at0; i < a.top; i += lanes_each) {
+        const float x = v[i];
+        if (!(x >= least) || x == kNegInf) break;  // they come in order
         const int at = atomicAdd(&kept, 1);
-        lv[at] = v[i];
+        lv[at] = x;
         li[at] = id[i];
     }
     __syncthreads();
-    for (int i = lane; i < kept; i += 64) {
-        int rank = 0;
-        for (int j = 0; j < kept; ++j) rank += before(lv[j], li[j], lv[i], li[i]) ? 1 : 0;
-        if (rank < a.top) write_top(a, row, rank, lv[i], li[i], e);
-    }
-    for (int r = kept + lane; r < a.top; r += 64) write_top(a, row, r, kNegInf, -1, e);
+    write_best(lv, li, kept, a.top, [&](int rank, float x, int i) { write_top(a, row, rank, x, i, e); });
 }
 
 // ---------------------------------------------------------------- gradient
@@ -570,21 +641,24 @@ __global__ __launch_bounds__(NT) void stats_grad_kernel(TokenStatsGrad a, int sp
 
 int64_t row_bytes(int64_t vocab, int32_t f32) { return vocab * (f32 ? 4 : 2); }
 
+template <int NT, int MODE>
+hipError_t launch_stats_mode(const TokenStats& a, hipStream_t s) {
+    const unsigned g = grid_of(a.rows * a.parts);
+    if (a.f32)
+        hipLaunchKernelGGL((stats_kernel<float, NT, MODE>), dim3(g), dim3(NT), 0, s, a);
+    else
+        hipLaunchKernelGGL((stats_kernel<uint16_t, NT, MODE>), dim3(g), dim3(NT), 0, s, a);
+    return hipGetLastError();
+}
+
+// The most pieces of any part are part_of()'s: whole lines of 8, behind up to
+// 7 pieces of the line that the row starts in.
 template <int NT>
 hipError_t launch_stats_nt(const TokenStats& a, hipStream_t s) {
-    const unsigned g = grid_of(a.rows * a.parts);
-    if (a.f32) {
-        if (a.top)
-            hipLaunchKernelGGL((stats_kernel<float, NT, true>), dim3(g), dim3(NT), 0, s, a);
-        else
-            hipLaunchKernelGGL((stats_kernel<float, NT, false>), dim3(g), dim3(NT), 0, s, a);
-    } else {
-        if (a.top)
-            hipLaunchKernelGGL((stats_kernel<uint16_t, NT, true>), dim3(g), dim3(NT), 0, s, a);
-        else
-            hipLaunchKernelGGL((stats_kernel<uint16_t, NT, false>), dim3(g), dim3(NT), 0, s, a);
-    }
-    return hipGetLastError();
+    if (a.top == 0) return launch_stats_mode<NT, TOP_NONE>(a, s);
+    const int64_t pieces = row_bytes(a.vocab, a.f32) / 16;
+    const int64_t most = a.parts == 1 ? pieces : ((pieces + 7 + a.parts - 1) / a.parts + 7) / 8 * 8;
+    return most <= kTake * NT ? launch_stats_mode<NT, TOP_HELD>(a, s) : launch_stats_mode<NT, TOP_LONG>(a, s);
 }
 
 // Rows of up to this many bytes take one wave each.
