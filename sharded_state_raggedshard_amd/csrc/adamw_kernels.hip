@@ -21,6 +21,7 @@
 
 #include "adamw.hpp"
 #include "kernel_common.hpp"
+#include "lanes.hpp"
 #include "raggedshard.h"
 
 namespace rs {
@@ -340,20 +341,15 @@ __global__ __launch_bounds__(NT) void step_kernel(const Tensor* __restrict__ ten
 
 // ------------------------------------------------------------ global norm
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-    return v;
-}
-
 // Sum over the workgroup in a fixed order; valid in thread 0.
+template <int THREADS>
 __device__ __forceinline__ double wg_sum(double v, double* lds) {
-    v = wave_sum(v);
+    v = lanes::sum64(v);
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
     double s = 0.0;
     if (threadIdx.x == 0)
-        for (int i = 0; i < NT / 64; ++i) s += lds[i];
+        for (int i = 0; i < THREADS / 64; ++i) s += lds[i];
     return s;
 }
 
@@ -388,16 +384,24 @@ __global__ __launch_bounds__(NT) void sumsq_kernel(const Tensor* __restrict__ te
         const int n = (int)(t.n - pos < kChunk ? t.n - pos : kChunk);
         sum += t.kind & KIND_GRAD_F32 ? sumsq_chunk<F32>(t, pos, n) : sumsq_chunk<BF16>(t, pos, n);
     }
-    sum = wg_sum(sum, lds);
+    sum = wg_sum<NT>(sum, lds);
     if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-__global__ __launch_bounds__(NT) void norm_kernel(const double* partial, int n, double* sumsq, double max_norm,
-                                                  float* scale) {
-    __shared__ double lds[NT / 64];
-    double sum = 0.0;
-    for (int i = threadIdx.x; i < n; i += NT) sum += partial[i];
-    sum = wg_sum(sum, lds);
+// The partial sums in a fixed order, all loads of a thread in flight at once.
+constexpr int kNormThreads = 512;
+__global__ __launch_bounds__(kNormThreads) void norm_kernel(const double* partial, int n, double* sumsq,
+                                                            double max_norm, float* scale) {
+    __shared__ double lds[kNormThreads / 64];
+    double x[kSumBlocks / kNormThreads], sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kSumBlocks / kNormThreads; ++i) {
+        const int at = i * kNormThreads + (int)threadIdx.x;
+        x[i] = at < n ? partial[at] : 0.0;
+    }
+#pragma unroll
+    for (int i = 0; i < kSumBlocks / kNormThreads; ++i) sum += x[i];
+    sum = wg_sum<kNormThreads>(sum, lds);
     if (threadIdx.x != 0) return;
     *sumsq = sum;
     if (scale) {
@@ -470,7 +474,7 @@ hipError_t launch_l2norm(const Work& w, double* partial, double* sumsq, double m
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(NT), 0, s, partial, n, sumsq, max_norm, scale);
+    hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(kNormThreads), 0, s, partial, n, sumsq, max_norm, scale);
     return hipGetLastError();
 }
 
