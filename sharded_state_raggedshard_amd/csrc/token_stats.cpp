@@ -91,7 +91,7 @@ rs_status rs_token_stats(const void* d_logits, int32_t dtype, int64_t rows, int6
     a.top_id = d_top_id;
     a.top_logp = d_top_logp;
     a.saved = d_saved;
-    a.parts = rs::stat_parts(rows, vocab);
+    a.parts = rs::stats_parts(rows, vocab);
     a.stat = reinterpret_cast<rs::PartStat*>(w);
     a.best = reinterpret_cast<float*>(w + sc.best);
     a.best_id = reinterpret_cast<int32_t*>(w + sc.best_id);

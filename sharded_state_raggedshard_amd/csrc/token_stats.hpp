@@ -12,11 +12,11 @@ namespace rs {
 
 constexpr int32_t kMaxTop = 32;
 
-// Statistics of a part of a row, without the row's token: its maximum, and the
-// sums of e = 2^d and e d over d = (z - m) k.
+// Statistics of a part of a row, without the row's token: the sums of e = 2^d
+// and e d over d = (z - m) k around a reference m; and the token's value.
 struct PartStat {
     double s, w;
-    float m, unused;
+    float m, token;
 };
 
 struct TokenStats {
@@ -38,8 +38,16 @@ struct TokenStats {
     int32_t* best_id;
 };
 
+// Parts that a row is split into: a power of two up to kMaxParts of at least
+// 4096 values each, kStatsItems parts of all rows together at most.
+constexpr int64_t kStatsItems = 512;
+inline int32_t stats_parts(int64_t rows, int64_t vocab) {
+    int32_t parts = 1;
+    while (rows > 0 && parts < kMaxParts && rows * 2 * parts <= kStatsItems && vocab >= 2 * parts * 4096) parts *= 2;
+    return parts;
+}
 // Parts of all rows of a call that splits its rows.
-inline int64_t stats_part_room(int64_t rows) { return std::min(rows * kMaxParts, kSplitItems); }
+inline int64_t stats_part_room(int64_t rows) { return std::min(rows * kMaxParts, kStatsItems); }
 
 struct TokenStatsGrad {
     const void* z;

@@ -106,12 +106,6 @@ __device__ __forceinline__ double log_p(const RowEnd& e, float v, float k) {
     return ((double)v - (double)e.m) * ((double)k * kLn2) - e.ln_s;
 }
 
-__device__ __forceinline__ bool takes_part(const TokenStats& a, int64_t row) {
-    if (!a.target) return true;
-    const int64_t y = a.target[row];
-    return y >= 0 && y < a.vocab;
-}
-
 // The outputs of a row but its alternatives, by one thread.
 __device__ __forceinline__ void write_row(const TokenStats& a, int64_t row, bool live, const RowEnd& e) {
     const bool none = !live || e.empty;
@@ -423,33 +417,42 @@ __global__ __launch_bounds__(NT, MODE == TOP_NONE ? 5 : 4) void stats_kernel(Tok
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
         const int64_t row = a.parts == 1 ? item : item / a.parts;
         const int index = (int)(item - row * a.parts);
-        if (!takes_part(a, row)) {
+        // the first loads need nothing but the row's place: they are under way
+        // while the token's index and value are fetched
+        const T* z = static_cast<const T*>(a.z) + row * a.ld;
+        const Pieces<T> ps(z, a.vocab);
+        const Part part = part_of(z, ps, index, a.parts);
+        const Segments<NT> seg(part);
+        const T* base = z + ps.head;
+        u32x4 raw[U];
+        const auto load = [&](int t) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int at = part.v0 + tid + (t * U + u) * NT;
+                raw[u] = Vec<T>::lowest();
+                if (at < part.v1) raw[u] = load16_once(base + at * N);
+            }
+        };
+        load(0);
+        const int64_t target = a.target ? a.target[row] : -1;
+        if (a.target && (target < 0 || target >= a.vocab)) {
             if (a.parts == 1 && tid < 64) {
                 if (tid == 0) write_row(a, row, false, RowEnd{});
                 if (TOP && tid < a.top) write_top(a, row, tid, 0.0f, -1, RowEnd{});
             }
             continue;
         }
-        const T* z = static_cast<const T*>(a.z) + row * a.ld;
-        const int y = a.target ? (int)a.target[row] : -1;
+        const int y = (int)target;
         const float token = y >= 0 ? Vec<T>::one(z[y]) : kNegInf;
-        const Pieces<T> ps(z, a.vocab);
-        const Part part = part_of(z, ps, index, a.parts);
-        const Segments<NT> seg(part);
         const Single<T> one(z, ps, part, y);
-        const T* base = z + ps.head;
         const int yv = ps.piece(y);
         Sums run{kNegInf, 0.0, 0.0};
         float ref = wave_uniform(token), best = kNegInf;
-        u32x4 raw[U] = {};
         for (int t = 0, next = seg.per, i = 0; t < seg.takes; ++t) {
-            const int v = part.v0 + tid + t * (U * NT);
+            if (t > 0) load(t);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                raw[u] = Vec<T>::lowest();
-                const int at = v + u * NT;
-                if (at < part.v1 && at != yv) raw[u] = load16_once(base + at * N);
-            }
+            for (int u = 0; u < U; ++u)
+                if (part.v0 + tid + (t * U + u) * NT == yv) raw[u] = Vec<T>::lowest();
             float x[U * N];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -500,7 +503,7 @@ __global__ __launch_bounds__(NT, MODE == TOP_NONE ? 5 : 4) void stats_kernel(Tok
             e = row_end(all, top, token, y >= 0, k);
             if (tid == 0) write_row(a, row, true, e);
         } else if (tid == 0) {
-            a.stat[item] = PartStat{all.s, all.w, top, 0.0f};
+            a.stat[item] = PartStat{all.s, all.w, top, token};
         }
         if (!TOP) continue;
         const int n = lds.c.n;
@@ -519,20 +522,24 @@ __global__ __launch_bounds__(NT, MODE == TOP_NONE ? 5 : 4) void stats_kernel(Tok
 // Rows in several parts: a wave joins a row's statistics, a lane a part, and
 // picks the best of its parts' best.
 constexpr int kMostBest = kMaxParts * kMaxTop;
-template <typename T>
 __global__ __launch_bounds__(64) void stats_join_kernel(TokenStats a) {
     __shared__ float lv[kMostBest];
     __shared__ int32_t li[kMostBest];
     __shared__ int32_t kept;
     const int lane = threadIdx.x;
     const int64_t row = blockIdx.x;
-    const bool live = takes_part(a, row);
+    // 64 / parts lanes a part, the first ones with its largest values.  All
+    // loads go out at once (of a row that takes no part they are of no use).
+    const int lanes_each = 64 / a.parts, at0 = lane % lanes_each;
+    const int64_t first = row * a.parts * a.top + (int64_t)(lane / lanes_each) * a.top;
+    const float* v = a.best + first;
+    const int32_t* id = a.best_id + first;
+    const float v0 = at0 < a.top ? v[at0] : kNegInf;
+    const PartStat p = a.stat[row * a.parts + lane % a.parts];
+    const int64_t y = a.target ? a.target[row] : -1;
+    const bool live = !a.target || (y >= 0 && y < a.vocab);
     RowEnd e{};
     if (live) {
-        const T* z = static_cast<const T*>(a.z) + row * a.ld;
-        const int64_t y = a.target ? a.target[row] : -1;
-        const float token = y >= 0 ? Vec<T>::one(z[y]) : kNegInf;
-        const PartStat p = a.stat[row * a.parts + lane % a.parts];
         const float top = wave_uniform(lanes::max<64>(p.m));
         Sums x{kNegInf, p.s, p.w};
         x.rescale(p.m, top == kNegInf ? 0.0f : top, a.k);
@@ -540,7 +547,7 @@ __global__ __launch_bounds__(64) void stats_join_kernel(TokenStats a) {
             x.s += __shfl_xor(x.s, off, 64);
             x.w += __shfl_xor(x.w, off, 64);
         }
-        e = row_end(x, top, token, y >= 0, a.k);
+        e = row_end(x, top, p.token, y >= 0, a.k);
     }
     if (lane == 0) write_row(a, row, live, e);
     if (a.top == 0) return;
@@ -548,13 +555,8 @@ __global__ __launch_bounds__(64) void stats_join_kernel(TokenStats a) {
         if (lane < a.top) write_top(a, row, lane, 0.0f, -1, e);
         return;
     }
-    // 64 / parts lanes a part, the first ones with its largest values: the
-    // n-th largest of the lanes' largest is reached by little more than n
-    const int lanes_each = 64 / a.parts, at0 = lane % lanes_each;
-    const int64_t first = row * a.parts * a.top + (int64_t)(lane / lanes_each) * a.top;
-    const float* v = a.best + first;
-    const int32_t* id = a.best_id + first;
-    const float least = nth_of_wave(at0 < a.top ? v[at0] : kNegInf, a.top);
+    // the n-th largest of the lanes' first values is reached by little more than n
+    const float least = nth_of_wave(v0, a.top);
     if (lane == 0) kept = 0;
     __syncthreads();
     for (int i = at0; i < a.top; i += lanes_each) {
@@ -672,10 +674,7 @@ hipError_t launch_token_stats(const TokenStats& a, hipStream_t s) {
     if (a.rows == 0) return hipSuccess;
     hipError_t e = row_bytes(a.vocab, a.f32) <= kWaveRow ? launch_stats_nt<64>(a, s) : launch_stats_nt<256>(a, s);
     if (e != hipSuccess || a.parts == 1) return e;
-    if (a.f32)
-        hipLaunchKernelGGL(stats_join_kernel<float>, dim3((unsigned)a.rows), dim3(64), 0, s, a);
-    else
-        hipLaunchKernelGGL(stats_join_kernel<uint16_t>, dim3((unsigned)a.rows), dim3(64), 0, s, a);
+    hipLaunchKernelGGL(stats_join_kernel, dim3((unsigned)a.rows), dim3(64), 0, s, a);
     return hipGetLastError();
 }
 
