@@ -211,19 +211,23 @@ def _ptr(x) -> Optional[int]:
 _current_device = None
 
 
-def _dev(x) -> Optional[int]:
-    """_ptr of a tensor that the current device holds: a launch there with
+def _devs(*xs):
+    """_ptr of tensors that the current device holds: a launch there with
     another one's memory, or the host's, could fault."""
     global _current_device
-    if x is None or isinstance(x, int):
-        return x
-    if _current_device is None:
-        import torch
-        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-    device = x.get_device()
-    if device < 0 or device != _current_device():
-        raise RaggedShardError(RS_EINVAL, f"a tensor on {x.device}, not on the current device")
-    return x.data_ptr()
+    out, current = [], None
+    for x in xs:
+        if x is not None and type(x) is not int:
+            if current is None:
+                if _current_device is None:
+                    import torch
+                    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+                current = _current_device() if x.is_cuda else -2
+            if x.get_device() != current:
+                raise RaggedShardError(RS_EINVAL, f"a tensor on {x.device}, not on the current device")
+            x = x.data_ptr()
+        out.append(x)
+    return out
 
 
 _current_stream = None
@@ -560,9 +564,10 @@ def rs_token_stats(logits, dtype: int, rows: int, vocab: int, ld: int, target, l
     """target (or None): int64 per row; logp, entropy (or None): fp32 per row;
     top_id: int64, top_logp: fp32 [rows, top] (None with top = 0); saved (or
     None): fp32 [rows, 4], for rs_token_stats_grad."""
-    _check(lib().rs_token_stats(_dev(logits), dtype, rows, vocab, ld, _dev(target), temperature,
-                                _dev(logp), _dev(entropy), top, _dev(top_id), _dev(top_logp),
-                                _dev(saved), _dev(work), nbytes, _stream(stream)))
+    logits, target, logp, entropy, top_id, top_logp, saved, work = _devs(
+        logits, target, logp, entropy, top_id, top_logp, saved, work)
+    _check(lib().rs_token_stats(logits, dtype, rows, vocab, ld, target, temperature, logp, entropy,
+                                top, top_id, top_logp, saved, work, nbytes, _stream(stream)))
 
 
 def rs_token_stats_grad(logits, dtype: int, rows: int, vocab: int, ld: int, target, saved, dlogp,
@@ -570,9 +575,10 @@ def rs_token_stats_grad(logits, dtype: int, rows: int, vocab: int, ld: int, targ
                         stream=None) -> None:
     """dlogp, dentropy (either may be None): fp32 per row; dlogits: as logits,
     row stride ldd."""
-    _check(lib().rs_token_stats_grad(_dev(logits), dtype, rows, vocab, ld, _dev(target),
-                                     temperature, _dev(saved), _dev(dlogp), _dev(dentropy),
-                                     _dev(dlogits), ldd, _stream(stream)))
+    logits, target, saved, dlogp, dentropy, dlogits = _devs(logits, target, saved, dlogp, dentropy,
+                                                            dlogits)
+    _check(lib().rs_token_stats_grad(logits, dtype, rows, vocab, ld, target, temperature, saved,
+                                     dlogp, dentropy, dlogits, ldd, _stream(stream)))
 
 
 def rs_expert_slots(rows: int, experts: int, k: int, align: int = 1) -> int:
@@ -594,8 +600,9 @@ def rs_expert_sort(topk, rows: int, experts: int, k: int, ldk: int, mask, align:
     """topk: int64 [rows, k] expert ids (row stride ldk); mask (or None): one
     byte per row; start: int64 [experts + 1]; count: int32 [experts]; slot:
     int32 [rows, k]."""
-    _check(lib().rs_expert_sort(_dev(topk), rows, experts, k, ldk, _dev(mask), align, _dev(start),
-                                _dev(count), _dev(slot), _dev(work), nbytes, _stream(stream)))
+    topk, mask, start, count, slot, work = _devs(topk, mask, start, count, slot, work)
+    _check(lib().rs_expert_sort(topk, rows, experts, k, ldk, mask, align, start, count, slot, work,
+                                nbytes, _stream(stream)))
 
 
 def rs_expert_dispatch(x, dtype: int, rows: int, hidden: int, ldx: int, slot, k: int, weight,
@@ -604,27 +611,28 @@ def rs_expert_dispatch(x, dtype: int, rows: int, hidden: int, ldx: int, slot, k:
     """x: [rows, hidden] to its slots' rows of y [slots, hidden]; weight (or
     None): fp32 [rows, k]; start and count (or both None: padding rows stay)
     from rs_expert_sort."""
-    _check(lib().rs_expert_dispatch(_dev(x), dtype, rows, hidden, ldx, _dev(slot), k, _dev(weight),
-                                    ldw, experts, _dev(start), _dev(count), _dev(y), slots, ldy,
-                                    _stream(stream)))
+    x, slot, weight, start, count, y = _devs(x, slot, weight, start, count, y)
+    _check(lib().rs_expert_dispatch(x, dtype, rows, hidden, ldx, slot, k, weight, ldw, experts,
+                                    start, count, y, slots, ldy, _stream(stream)))
 
 
 def rs_expert_combine(y, dtype: int, slots: int, hidden: int, ldy: int, slot, rows: int, k: int,
                       weight, ldw: int, add, lda: int, out, ldo: int, stream=None) -> None:
     """out [rows, hidden] = add (or None) + the weighted sum of the slots'
     rows of y [slots, hidden]; weight (or None): fp32 [rows, k]."""
-    _check(lib().rs_expert_combine(_dev(y), dtype, slots, hidden, ldy, _dev(slot), rows, k,
-                                   _dev(weight), ldw, _dev(add), lda, _dev(out), ldo,
-                                   _stream(stream)))
+    y, slot, weight, add, out = _devs(y, slot, weight, add, out)
+    _check(lib().rs_expert_combine(y, dtype, slots, hidden, ldy, slot, rows, k, weight, ldw, add,
+                                   lda, out, ldo, _stream(stream)))
 
 
 def rs_expert_combine_grad(dout, dtype: int, rows: int, hidden: int, ldo: int, y, slots: int,
                            ldy: int, slot, k: int, weight, ldw: int, experts: int, start, count, dy,
                            lddy: int, dweight, lddw: int, stream=None) -> None:
     """dy (or None): [slots, hidden], may be y; dweight: fp32 [rows, k]."""
-    _check(lib().rs_expert_combine_grad(_dev(dout), dtype, rows, hidden, ldo, _dev(y), slots, ldy,
-                                        _dev(slot), k, _dev(weight), ldw, experts, _dev(start),
-                                        _dev(count), _dev(dy), lddy, _dev(dweight), lddw,
+    dout, y, slot, weight, start, count, dy, dweight = _devs(dout, y, slot, weight, start, count, dy,
+                                                             dweight)
+    _check(lib().rs_expert_combine_grad(dout, dtype, rows, hidden, ldo, y, slots, ldy, slot, k,
+                                        weight, ldw, experts, start, count, dy, lddy, dweight, lddw,
                                         _stream(stream)))
 
 
@@ -648,7 +656,7 @@ def rs_adamw_device_bytes(adamw: int) -> int:
 
 
 def rs_adamw_upload(adamw: int, workspace, nbytes: int, stream=None) -> None:
-    _check(lib().rs_adamw_upload(adamw, _dev(workspace), nbytes, _stream(stream)))
+    _check(lib().rs_adamw_upload(adamw, *_devs(workspace), nbytes, _stream(stream)))
 
 
 def rs_adamw_bind(adamw: int, params: Sequence, grads: Sequence, m: Sequence, v: Sequence,
@@ -661,26 +669,26 @@ def rs_adamw_bind(adamw: int, params: Sequence, grads: Sequence, m: Sequence, v:
             return None
         if len(xs) != len(params):
             raise ValueError("the lists differ in length")
-        return (C.c_void_p * len(xs))(*[_dev(x) for x in xs])
+        return (C.c_void_p * len(xs))(*_devs(*xs))
     _check(lib().rs_adamw_bind(adamw, *[table(x) for x in (params, grads, m, v, amax_m, amax_v,
                                                            bf16_out)], _stream(stream)))
 
 
 def rs_adamw_l2norm_clip(adamw: int, max_norm: float, sumsq, scale=None, stream=None) -> None:
-    _check(lib().rs_adamw_l2norm_clip(adamw, max_norm, _dev(sumsq), _dev(scale), _stream(stream)))
+    _check(lib().rs_adamw_l2norm_clip(adamw, max_norm, *_devs(sumsq, scale), _stream(stream)))
 
 
 def rs_adamw_step(adamw: int, hparams: Sequence, grad_scale=None, stream=None) -> None:
     """hparams: rs_adam_hparams, or dicts of its fields, one per group."""
     hp = (rs_adam_hparams * len(hparams))(*[h if isinstance(h, rs_adam_hparams)
                                             else rs_adam_hparams(**h) for h in hparams])
-    _check(lib().rs_adamw_step(adamw, hp, len(hparams), _dev(grad_scale), _stream(stream)))
+    _check(lib().rs_adamw_step(adamw, hp, len(hparams), *_devs(grad_scale), _stream(stream)))
 
 
 def rs_adamw_moments(adamw: int, m, v, dtype: int = RS_F32, stream=None) -> None:
     """m, v (either may be None): every tensor's moments as `dtype` values,
     one tensor behind the other."""
-    _check(lib().rs_adamw_moments(adamw, _dev(m), _dev(v), dtype, _stream(stream)))
+    _check(lib().rs_adamw_moments(adamw, *_devs(m, v), dtype, _stream(stream)))
 
 
 def rs_last_error() -> str:
