@@ -369,18 +369,24 @@ rs_status rs_adam8_step_fp8(const rs_plan* plan, int32_t bucket, int32_t rank, f
  *   m = (q_m / 127) amax_m, q_m = rne(m / amax_m * 127),
  *   v = (q_v / 255) amax_v, q_v = rne(v / amax_v * 255)  (0 if amax 0),
  * the new parameters coming from the new moments before they are quantised.
- * Codes and absmax equal rs_adam8_step's bit for bit.  Non-finite gradients
- * give unspecified values (as there), in their own tensor only. */
+ * Codes and absmax equal rs_adam8_step's bit for bit.  They keep a v below
+ * amax / 510 as 0, and an element whose m is kept and whose v is not can take
+ * a step far beyond lr where its next gradient is small; RS_STATE_INT8_ROOT
+ * codes the root instead,
+ *   v = (q_v / 255)^2 amax_v, q_v = rne(sqrt(v / amax_v) * 255), at least 1
+ *                                   where v > 0,
+ * for blocks whose gradients differ widely (rows that few tokens reach).
+ * Non-finite gradients give unspecified values, in their own tensor only. */
 typedef struct rs_adamw rs_adamw; /* opaque, host-owned */
 
-enum { RS_STATE_F32 = 0, RS_STATE_INT8 = 1 };
+enum { RS_STATE_F32 = 0, RS_STATE_INT8 = 1, RS_STATE_INT8_ROOT = 2 };
 
 typedef struct {
     int64_t numel;    /* >= 0 */
     int32_t param;    /* RS_F32 or RS_BF16 */
     int32_t grad;     /* RS_F32 or RS_BF16 */
     int32_t state;    /* RS_STATE_* */
-    int32_t block;    /* RS_STATE_INT8: a power of two in 64..4096, else 0 */
+    int32_t block;    /* 8-bit states: a power of two in 64..4096, else 0 */
     int32_t group;    /* its hyper-parameters' index in rs_adamw_step, 0..15 */
     int32_t reserved; /* must be 0 */
 } rs_adamw_tensor;
@@ -405,7 +411,7 @@ rs_status rs_adamw_upload(rs_adamw* adamw, void* d_workspace, size_t bytes, void
 /* Where the tensors' arrays are: host arrays of n device pointers each, all
  * aligned to their elements.  d_m, d_v: binary32 moments, or int8 / uint8
  * codes; d_amax_m, d_amax_v: ceil(numel / block) floats (read only for
- * RS_STATE_INT8 tensors; the arrays may be NULL without any); d_bf16_out
+ * tensors with 8-bit states; the arrays may be NULL without any); d_bf16_out
  * (nullable, entries too): bf16_rne of the new binary32 parameters.  An empty
  * tensor's pointers are not looked at.  No written array shares a byte with
  * another array (RS_EINVAL).  May be called again, as when gradients move;

@@ -29,7 +29,7 @@ RS_ALIGN_CUT_UNIT = 0x100
 RS_SPLIT_TWO_PASS, RS_SPLIT_COOPERATIVE, RS_SPLIT_ORDERED = 0, 1, 2
 RS_PREF_SIGMOID, RS_PREF_HINGE, RS_PREF_IPO = 0, 1, 2
 RS_SCORE_SOFTMAX, RS_SCORE_SIGMOID = 0, 1
-RS_STATE_F32, RS_STATE_INT8 = 0, 1
+RS_STATE_F32, RS_STATE_INT8, RS_STATE_INT8_ROOT = 0, 1, 2
 RS_ALL = -1
 
 # every entry point declared in include/raggedshard.h
@@ -800,7 +800,7 @@ class AdamW:
             raise RaggedShardError(RS_EINVAL, f"{n} entries per list needed")
         sizes = {RS_F32: 4, RS_BF16: 2}
         for i, (numel, p, g, state, block, _) in enumerate(self.tensors):
-            eight = state == RS_STATE_INT8
+            eight = state != RS_STATE_F32
             blocks = -(-numel // block) if eight else 0
             each = ((params, numel, sizes[p]), (grads, numel, sizes[g]), (m, numel, 1 if eight else 4),
                     (v, numel, 1 if eight else 4), (amax_m, blocks, 4), (amax_v, blocks, 4),

@@ -45,9 +45,10 @@ rs_status check_tensor(const rs_adamw_tensor& t) {
     if (t.numel > rs::aw::kMaxElems) return fail(RS_EOVERFLOW, "a tensor beyond 2^42 elements");
     if ((t.param != RS_F32 && t.param != RS_BF16) || (t.grad != RS_F32 && t.grad != RS_BF16))
         return fail(RS_EINVAL, "unknown dtype");
-    if (t.state != RS_STATE_F32 && t.state != RS_STATE_INT8) return fail(RS_EINVAL, "unknown state");
+    if (t.state != RS_STATE_F32 && t.state != RS_STATE_INT8 && t.state != RS_STATE_INT8_ROOT)
+        return fail(RS_EINVAL, "unknown state");
     if (t.state == RS_STATE_F32 && t.block != 0) return fail(RS_EINVAL, "binary32 moments have no blocks");
-    if (t.state == RS_STATE_INT8 &&
+    if (t.state != RS_STATE_F32 &&
         (t.block < (1 << rs::aw::kMinBlockLog2) || t.block > (1 << rs::aw::kMaxBlockLog2) ||
          (t.block & (t.block - 1)) != 0))
         return fail(RS_EINVAL, "block must be a power of two in 64..4096");
@@ -107,7 +108,7 @@ rs_status bind(rs_adamw* h, void* const* d_param, const void* const* d_grad, voi
     int64_t first = 0;
     for (size_t i = 0; i < n; ++i) {
         const rs_adamw_tensor& t = h->tensors[i];
-        const bool eight = t.state == RS_STATE_INT8;
+        const bool eight = t.state != RS_STATE_F32;
         const int64_t psize = t.param == RS_F32 ? 4 : 2, gsize = t.grad == RS_F32 ? 4 : 2, ssize = eight ? 1 : 4;
         rs::aw::Tensor& d = table[i];
         d = rs::aw::Tensor{};
@@ -119,7 +120,7 @@ rs_status bind(rs_adamw* h, void* const* d_param, const void* const* d_grad, voi
         d.n = t.numel;
         d.first = first;
         d.kind = (t.param == RS_F32 ? rs::aw::KIND_PARAM_F32 : 0) | (t.grad == RS_F32 ? rs::aw::KIND_GRAD_F32 : 0) |
-                 (eight ? rs::aw::KIND_INT8 : 0);
+                 (eight ? rs::aw::KIND_INT8 : 0) | (t.state == RS_STATE_INT8_ROOT ? rs::aw::KIND_ROOT : 0);
         d.block_log2 = eight ? block_log2(t) : 0;
         d.group = t.group;
         first += t.numel;
@@ -193,7 +194,7 @@ rs_status rs_adamw_plan(const rs_adamw_tensor* tensors, int32_t n, rs_adamw** ou
         for (int32_t i = 0; i < n; ++i) {
             for (int64_t c = 0; c < ceil_div(tensors[i].numel, kChunk); ++c) h->chunks.push_back({i, (int32_t)c});
             h->n_groups = std::max(h->n_groups, tensors[i].group + 1);
-            h->int8 = h->int8 || tensors[i].state == RS_STATE_INT8;
+            h->int8 = h->int8 || tensors[i].state != RS_STATE_F32;
         }
     } catch (const std::bad_alloc&) {
         delete h;

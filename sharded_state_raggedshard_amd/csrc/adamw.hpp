@@ -34,7 +34,7 @@ struct alignas(16) Tensor {
 };
 static_assert(sizeof(Tensor) == 96, "Tensor layout");
 
-enum { KIND_PARAM_F32 = 1, KIND_GRAD_F32 = 2, KIND_INT8 = 4 };
+enum { KIND_PARAM_F32 = 1, KIND_GRAD_F32 = 2, KIND_INT8 = 4, KIND_ROOT = 8 };
 
 // Elements [kChunk * index, kChunk * (index + 1)) of a tensor.
 struct Chunk {

@@ -1,7 +1,8 @@
 // AdamW over many tensors in one launch, for gfx950: binary32 moments, or the
 // 8-bit ones of the blockwise-int8 step (one binary32 absmax per block, m as
-// int8 over 127 levels, v as uint8 over 255 levels), master parameters in
-// binary32 (with a bf16 copy beside them where asked) or bf16 parameters.
+// int8 over 127 levels, v as uint8 over 255 levels) or those with the root of v
+// in its place, master parameters in binary32 (with a bf16 copy beside them
+// where asked) or bf16 parameters.
 //
 // One workgroup takes a chunk of 4096 elements of one tensor from a work
 // table.  A lane owns 16 elements: wave w covers [1024 w, 1024 (w + 1)) of the
@@ -149,8 +150,11 @@ __device__ __forceinline__ void give(typename A::type* p, int at, int count, con
 __device__ __forceinline__ float level_m(uint32_t code) {
     return kc::ratio_fast((float)(int8_t)(uint8_t)code, 127.0f, 1.0f / 127.0f);
 }
-__device__ __forceinline__ float level_v(uint32_t code) {
-    return kc::ratio_fast((float)code, 255.0f, 1.0f / 255.0f);
+// The second moment's codes are of v / absmax, or of its square root: then an
+// element is kept down to 1 / 260,000 of its block's largest instead of 1 / 510.
+__device__ __forceinline__ float level_v(uint32_t code, bool root) {
+    const float x = kc::ratio_fast((float)code, 255.0f, 1.0f / 255.0f);
+    return root ? x * x : x;
 }
 
 // New parameters of four elements from their new moments: the hardware square
@@ -175,7 +179,8 @@ __device__ __forceinline__ void new_params(const StepScalars& sc, const float (&
 }
 
 // Codes of four elements of one block.  |m| <= absmax bounds them; int8 by a
-// +128 offset.
+// +128 offset.  A code of a square root is 0 only for 0.
+template <bool ROOT>
 __device__ __forceinline__ void quantise(const float* m, const float* v, float am, float av, uint32_t& qm,
                                          uint32_t& qv) {
     const float ym = kc::quant_recip(am), yv = kc::quant_recip(av);
@@ -187,7 +192,9 @@ __device__ __forceinline__ void quantise(const float* m, const float* v, float a
         if (__builtin_expect(slow_m, 0)) rm = m[j] / am;
         if (__builtin_expect(slow_v, 0)) rv = v[j] / av;
         qm = __builtin_amdgcn_cvt_pk_u8_f32(rintf(rm * 127.0f) + 128.0f, j, qm);
-        qv = __builtin_amdgcn_cvt_pk_u8_f32(rintf(rv * 255.0f), j, qv);
+        float cv = rintf((ROOT ? sqrtf(rv) : rv) * 255.0f);
+        if (ROOT && v[j] > 0.0f) cv = fmaxf(cv, 1.0f);
+        qv = __builtin_amdgcn_cvt_pk_u8_f32(cv, j, qv);
     }
     qm ^= 0x80808080u;
 }
@@ -236,9 +243,13 @@ __device__ __forceinline__ void block_max(float (&am)[KG], float (&av)[KG], int 
     }
 }
 
-template <typename P, typename G, bool INT8>
+// How the moments are kept.
+enum { STATE_F32, STATE_INT8, STATE_ROOT };
+
+template <typename P, typename G, int STATE>
 __device__ __forceinline__ void step_chunk(const Tensor& t, const StepScalars& sc, float s, int64_t pos, int n,
                                            float (*red)[2]) {
+    constexpr bool INT8 = STATE != STATE_F32, ROOT = STATE == STATE_ROOT;
     using S = typename std::conditional<INT8, Code, F32>::type;
     typename P::type* param = static_cast<typename P::type*>(t.param) + pos;
     const typename G::type* grad = static_cast<const typename G::type*>(t.grad) + pos;
@@ -269,7 +280,7 @@ __device__ __forceinline__ void step_chunk(const Tensor& t, const StepScalars& s
             float mh, vh;
             if constexpr (INT8) {
                 mh = level_m((rm[k] >> (8 * j)) & 0xffu) * am[k];
-                vh = level_v((rv[k] >> (8 * j)) & 0xffu) * av[k];
+                vh = level_v((rv[k] >> (8 * j)) & 0xffu, ROOT) * av[k];
             } else {
                 mh = F32::get(rm[k], j);
                 vh = F32::get(rv[k], j);
@@ -305,7 +316,7 @@ __device__ __forceinline__ void step_chunk(const Tensor& t, const StepScalars& s
         for (int k = 0; k < KG; ++k) {
             const int at = slice_at(k), count = slice_count(k, n);
             uint32_t qm, qv;
-            quantise(M + 4 * k, V + 4 * k, am[k], av[k], qm, qv);
+            quantise<ROOT>(M + 4 * k, V + 4 * k, am[k], av[k], qm, qv);
             give<Code>(m, at, count, qm);
             give<Code>(v, at, count, qv);
             if (count && (at & ((1 << t.block_log2) - 1)) == 0) {
@@ -314,6 +325,17 @@ __device__ __forceinline__ void step_chunk(const Tensor& t, const StepScalars& s
                 global<float>(t.amax_v)[blk] = av[k];
             }
         }
+    }
+}
+
+template <int STATE>
+__device__ __forceinline__ void step_types(const Tensor& t, const StepScalars& g, float s, int64_t pos, int n,
+                                           float (*red)[2]) {
+    switch (t.kind & (KIND_PARAM_F32 | KIND_GRAD_F32)) {
+    case 0: step_chunk<BF16, BF16, STATE>(t, g, s, pos, n, red); break;
+    case KIND_PARAM_F32: step_chunk<F32, BF16, STATE>(t, g, s, pos, n, red); break;
+    case KIND_GRAD_F32: step_chunk<BF16, F32, STATE>(t, g, s, pos, n, red); break;
+    default: step_chunk<F32, F32, STATE>(t, g, s, pos, n, red); break;
     }
 }
 
@@ -328,16 +350,12 @@ __global__ __launch_bounds__(NT) void step_kernel(const Tensor* __restrict__ ten
         const int64_t pos = (int64_t)ch.index * kChunk;
         const int n = (int)(t.n - pos < kChunk ? t.n - pos : kChunk);
         const StepScalars& g = sc.group[t.group];
-        switch (t.kind) {
-        case 0: step_chunk<BF16, BF16, false>(t, g, s, pos, n, red); break;
-        case KIND_PARAM_F32: step_chunk<F32, BF16, false>(t, g, s, pos, n, red); break;
-        case KIND_GRAD_F32: step_chunk<BF16, F32, false>(t, g, s, pos, n, red); break;
-        case KIND_PARAM_F32 | KIND_GRAD_F32: step_chunk<F32, F32, false>(t, g, s, pos, n, red); break;
-        case KIND_INT8: step_chunk<BF16, BF16, true>(t, g, s, pos, n, red); break;
-        case KIND_INT8 | KIND_PARAM_F32: step_chunk<F32, BF16, true>(t, g, s, pos, n, red); break;
-        case KIND_INT8 | KIND_GRAD_F32: step_chunk<BF16, F32, true>(t, g, s, pos, n, red); break;
-        default: step_chunk<F32, F32, true>(t, g, s, pos, n, red); break;
-        }
+        if (!(t.kind & KIND_INT8))
+            step_types<STATE_F32>(t, g, s, pos, n, red);
+        else if (!(t.kind & KIND_ROOT))
+            step_types<STATE_INT8>(t, g, s, pos, n, red);
+        else
+            step_types<STATE_ROOT>(t, g, s, pos, n, red);
     }
 }
 
@@ -436,7 +454,7 @@ __device__ __forceinline__ void moments_chunk(const Tensor& t, int64_t pos, int 
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint32_t c = (r >> (8 * j)) & 0xffu;
-                x[j] = (second ? level_v(c) : level_m(c)) * a;
+                x[j] = (second ? level_v(c, t.kind & KIND_ROOT) : level_m(c)) * a;
             }
         } else {
             const u32x4 r = take<F32>(static_cast<const float*>(second ? t.v : t.m) + pos, at, count);

@@ -32,7 +32,7 @@ def handles():
         rs.rs_adamw_free(h)
 
 
-@pytest.mark.parametrize("at,value", [(0, -1), (1, 2), (2, -1), (3, 2), (4, 64), (5, -1), (5, 16)])
+@pytest.mark.parametrize("at,value", [(0, -1), (1, 2), (2, -1), (3, 3), (3, -1), (4, 64), (5, -1), (5, 16)])
 def test_bad_tensors(at, value):
     t = list(OK)
     t[at] = value
@@ -41,7 +41,8 @@ def test_bad_tensors(at, value):
 
 @pytest.mark.parametrize("block", [0, 1, 32, 63, 96, 4095, 8192, -256])
 def test_bad_blocks(block):
-    assert status(rs.rs_adamw_plan, [(1000, F32, F32, rs.RS_STATE_INT8, block, 0)]) == rs.RS_EINVAL
+    for state in (rs.RS_STATE_INT8, rs.RS_STATE_INT8_ROOT):
+        assert status(rs.rs_adamw_plan, [(1000, F32, F32, state, block, 0)]) == rs.RS_EINVAL
 
 
 def test_sizes():

@@ -391,3 +391,88 @@ def test_offsets_beyond_32_bits(block, numel):
                       m=[torch.zeros(n, **dev)], v=[torch.zeros(n, **dev)], amax_m=[torch.zeros(1, **dev)], amax_v=[torch.zeros(1, **dev)])
         check([(n, BF16, BF16, state, block, 0)], before, part, [hp], 1.0, f"at {w}")
     h.free()
+
+
+ROOT = rs.RS_STATE_INT8_ROOT
+
+
+@pytest.mark.parametrize("block", [64, 256, 1024, 4096])
+@pytest.mark.parametrize("p,g", [(F32, BF16), (BF16, F32)])
+def test_root_codes_against_binary64(block, p, g):
+    """The second moment by its root: v0 = (q / 255)^2 amax takes two products
+    and a quotient more (2 u), the rest as above; the root of a quotient off by
+    r of itself is off by r / 2, and a u more."""
+    log(f"adamw root codes {block} {p} {g}")
+    for aligned in (True, False):
+        tensors = [(n, p, g, ROOT, block, i % 2) for i, n in enumerate(SIZES)]
+        as_codes = [(n, p, g, rs.RS_STATE_INT8, block, i % 2) for i, n in enumerate(SIZES)]
+        h, a, store = make(as_codes, 40 + block, aligned, out=True)
+        h.free()
+        h = rs.AdamW(tensors).upload().bind(**a)
+        hps = [HP, {**HP, "beta2": 0.95, "weight_decay": 0.0, "step": 1}]
+        for turn in range(2):
+            before = clone(a)
+            h.step(hps)
+            for i, (numel, _, _, _, _, group) in enumerate(tensors):
+                if numel == 0:
+                    continue
+                hp = hps[group]
+                b1, b2, t = hp["beta1"], hp["beta2"], hp["step"]
+                gr = before["grads"][i].double()
+                m0 = before["m"][i].double() * spread(before["amax_m"][i], block, numel) / 127
+                v0 = (before["v"][i].double() / 255) ** 2 * spread(before["amax_v"][i], block, numel)
+                m, v = b1 * m0 + (1 - b1) * gr, b2 * v0 + (1 - b2) * gr * gr
+                em, ev = 7 * U * (b1 * m0.abs() + (1 - b1) * gr.abs()), 12 * U * v
+                den = v.sqrt() / math.sqrt(1 - b2 ** t) + hp["eps"]
+                size = hp["lr"] / (1 - b1 ** t)
+                step = size * m / den
+                th0 = before["params"][i].double()
+                th = th0 * (1 - hp["lr"] * hp["weight_decay"]) - step
+                tol = size * em / den + 17 * U * step.abs() + 3 * U * (th0.abs() + step.abs()) + (2.0 ** -8 * th.abs() if p == BF16 else 0.0)
+                assert ((a["params"][i].double() - th).abs() <= tol).all(), (numel, turn)
+                pad = -numel % block
+                top = torch.nn.functional.pad(v, (0, pad)).view(-1, block).amax(1)
+                assert ((a["amax_v"][i].double() - top).abs() <= 12 * U * top).all()
+                at = spread(top, block, numel)
+                ideal = torch.where(at > 0, (v / at).sqrt() * 255, 0.0)
+                code = a["v"][i].double()
+                near = ((code - ideal).abs() <= 0.5 + (12 + 12 + 4) * U * 255) | ((code == 1) & (ideal < 1) & (v > 0))
+                assert near.all() and (code[v > 0] > 0).all(), (numel, turn)
+        assert store.intact()
+        total = sum(SIZES)
+        out = torch.zeros(total, device="cuda")
+        h.moments(None, out, F32)
+        at = 0
+        for i, n in enumerate(SIZES):
+            x = (a["v"][i].double() / 255).float()
+            assert torch.equal(out[at:at + n], (x * x) * a["amax_v"][i].repeat_interleave(block)[:n]), n
+            at += n
+        h.free()
+
+
+def test_root_codes_hold_what_linear_ones_lose():
+    """Elements whose gradients pause after a hundredth of the block's largest:
+    their v survives, so their steps stay near lr; kept states change nothing
+    where no gradient comes."""
+    log("adamw root codes, rare rows")
+    n, block = 4096, 256
+    g = torch.full((n,), 1.0, device="cuda")
+    g[::2] = 1e-2
+    arrays = dict(params=[torch.zeros(n, device="cuda")], grads=[g], m=[torch.zeros(n, dtype=torch.int8, device="cuda")],
+                  v=[torch.zeros(n, dtype=torch.uint8, device="cuda")], amax_m=[torch.zeros(n // block, device="cuda")],
+                  amax_v=[torch.zeros(n // block, device="cuda")], bf16_out=[None])
+    h = rs.AdamW([(n, F32, F32, ROOT, block, 0)]).upload().bind(**arrays)
+    hp = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0)
+    h.step([{**hp, "step": 1}])
+    assert (arrays["v"][0][::2] == 3).all()  # 255 / 100, to the nearest
+    arrays["grads"][0].zero_()
+    before = arrays["params"][0].clone()
+    h.step([{**hp, "step": 2}])
+    move = (arrays["params"][0] - before).abs()
+    # m / sqrt(v) is within (1 / 127 / 0.01 / 2 and 3 / 2.55 - 1, together a factor 2) of 1
+    assert (move < 2e-3).all() and (move[::2] > 2e-4).all()
+    codes = arrays["v"][0].clone()
+    for t in range(3, 40):  # v shrinks everywhere alike: its codes stay
+        h.step([{**hp, "step": t}])
+    assert torch.equal(arrays["v"][0], codes)
+    h.free()
