@@ -5,14 +5,18 @@
 Plans three tensors over m = 4 ranks: the output head of a tiny model and a
 router in one bucket (matrices in 128 x 128 tiles), the head's bias in
 another (a vector in 32-element blocks); neither bucket needs padding.
-Copies fp32 master parameters in, and runs a few steps of: the losses on
-random hidden states with their logits' gradients (a preference loss on
-packed pairs in the first step, a clipped policy loss with a KL term after
-it; the router's balance loss in each), the parameters' gradients into the
-grad DBuffer, global L2 norm with the clipping coefficient, the
+Copies fp32 master parameters in, and runs a few steps of: the tokens of
+random hidden states sorted by the router's choices, carried to the experts
+(each scales its rows) and back with their weights, the losses on what comes
+out with their logits' gradients (a preference loss on packed pairs in the
+first step, a clipped policy loss with a KL term in the second, a weighted
+log-probability with an entropy bonus from then on; the router's balance loss
+in each), the way back through the experts, the parameters' gradients into
+the grad DBuffer, global L2 norm with the clipping coefficient, the
 blockwise-int8 AdamW step of rank `rank` (grad scale = the coefficient, bf16
 copy-in of the new parameters fused), zeroing of the gradients, copy-out to
-per-parameter bf16 views.  On m GPUs each rank would run the same calls on
+per-parameter bf16 views; and, for the experts' scales and a scale of the
+hidden states, which no plan holds, an AdamW step over both tensors.  On m GPUs each rank would run the same calls on
 its own slices and an AllGather / ReduceScatter would move the bf16 buffer
 between them; on one GPU every rank's slice lives in the same arrays.
 """
@@ -24,7 +28,7 @@ import sharded_state_raggedshard_amd as rs
 from synth import ROWS, TILE, TensorSpec
 
 
-TOKENS, TOPK, PAIRS = 96, 4, 4
+TOKENS, TOPK, PAIRS, ALTERNATIVES, TILE_ROWS = 96, 4, 4, 5, 2
 
 
 def main(steps: int = 3, rank: int = rs.RS_ALL) -> dict:
@@ -62,22 +66,56 @@ def main(steps: int = 3, rank: int = rs.RS_ALL) -> dict:
     counts = torch.zeros(experts, dtype=torch.int32, device=dev)
     mean_prob = torch.zeros(experts, device=dev)
     policy_stats, pair_stats, router_stats = (torch.zeros(n, device=dev) for n in (4, 3, 2))
+    entropy, saved = torch.zeros(TOKENS, device=dev), torch.zeros(TOKENS, 4, device=dev)
+    top_id = torch.zeros(TOKENS, ALTERNATIVES, dtype=torch.int64, device=dev)
+    top_logp = torch.zeros(TOKENS, ALTERNATIVES, device=dev)
     nbytes = max(rs.rs_objective_bytes(TOKENS, vocab, 2 * PAIRS),
-                 rs.rs_router_balance_bytes(TOKENS, experts))
+                 rs.rs_router_balance_bytes(TOKENS, experts),
+                 rs.rs_token_stats_bytes(TOKENS, vocab, ALTERNATIVES),
+                 rs.rs_expert_sort_bytes(TOKENS, experts, TOPK))
     work = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     start = torch.arange(2 * PAIRS + 1, device=dev) * (TOKENS // (2 * PAIRS))
     weight = torch.full((TOKENS,), 1.0 / TOKENS, device=dev)
+    # the sorted tokens, in tiles of rows per expert, and their gradients
+    slots = rs.rs_expert_slots(TOKENS, experts, TOPK, TILE_ROWS)
+    first = torch.zeros(experts + 1, dtype=torch.int64, device=dev)
+    taken = torch.zeros(experts, dtype=torch.int32, device=dev)
+    slot = torch.zeros(TOKENS, TOPK, dtype=torch.int32, device=dev)
+    rows, drows = torch.zeros(slots, 512, device=dev), torch.zeros(slots, 512, device=dev)
+    mixed, dx = torch.zeros(TOKENS, 512, device=dev), torch.zeros(TOKENS, 512, device=dev)
+    dgate = torch.zeros(TOKENS, TOPK, device=dev)
+    # parameters of no plan: the experts' scales with 8-bit moments, a scale of
+    # the hidden states with binary32 ones and no weight decay
+    scales = [torch.ones(experts, 512, device=dev), torch.ones(512, device=dev)]
+    dscales = [torch.zeros_like(p) for p in scales]
+    adamw = rs.AdamW([(experts * 512, rs.RS_F32, rs.RS_F32, rs.RS_STATE_INT8_ROOT, 256, 0),
+                      (512, rs.RS_F32, rs.RS_F32, rs.RS_STATE_F32, 0, 1)]).upload()
+    adamw.bind(scales, dscales,
+               [torch.zeros(experts * 512, dtype=torch.int8, device=dev), torch.zeros(512, device=dev)],
+               [torch.zeros(experts * 512, dtype=torch.uint8, device=dev), torch.zeros(512, device=dev)],
+               [torch.zeros(experts * 2, device=dev), None], [torch.zeros(experts * 2, device=dev), None])
+    other_sumsq, other_clip = torch.zeros(1, dtype=torch.float64, device=dev), torch.zeros(1, device=dev)
     for t in range(1, steps + 1):
         # forward pass of the tiny model on random hidden states
         w, router, b = (v.view(torch.bfloat16).float() for v in weights)
         w, router = w.view(vocab, 512), router.view(experts, 512)
-        x = torch.randn(TOKENS, 512, device=dev)
-        logits, scores = x @ w.T + b, x @ router.T
+        hidden = torch.randn(TOKENS, 512, device=dev)
+        x = hidden * scales[1]
+        scores = x @ router.T
+        values, topk = scores.topk(TOPK)
+        gate = torch.softmax(values, -1)
+        rs.rs_expert_sort(topk, TOKENS, experts, TOPK, TOPK, None, TILE_ROWS, first, taken, slot, work, nbytes)
+        rs.rs_expert_dispatch(x, rs.RS_F32, TOKENS, 512, 512, slot, TOPK, None, 0, experts, first, taken, rows, slots,
+                              512)
+        of = torch.searchsorted(first[1:], torch.arange(slots, device=dev), right=True).clamp(max=experts - 1)
+        made = rows * scales[0][of]  # the experts: a row of each one's tile times its scales
+        rs.rs_expert_combine(made, rs.RS_F32, slots, 512, 512, slot, TOKENS, TOPK, gate, TOPK, x, 512, mixed, 512)
+        logits = mixed @ w.T + b
         target = torch.randint(0, vocab, (TOKENS,), device=dev)
         if t == 1:
             rs.rs_preference_loss(logits, rs.RS_F32, TOKENS, vocab, vocab, target, start, PAIRS,
                                   None, None, dlogits, vocab, seq_logp, pair_stats, work, nbytes)
-        else:
+        elif t == 2:
             rs.rs_token_logp(logits, rs.RS_F32, TOKENS, vocab, vocab, target, old_logp, work,
                              nbytes)
             ref_logp.copy_(old_logp).add_(0.1 * torch.randn(TOKENS, device=dev))
@@ -85,17 +123,37 @@ def main(steps: int = 3, rank: int = rs.RS_ALL) -> dict:
             rs.rs_policy_loss(logits, rs.RS_F32, TOKENS, vocab, vocab, target, old_logp, ref_logp,
                               advantage, weight, dlogits, vocab, logp, policy_stats, work, nbytes,
                               kl_coef=0.05)
-        topk = scores.topk(TOPK).indices
+        else:
+            rs.rs_token_stats(logits, rs.RS_F32, TOKENS, vocab, vocab, target, logp, entropy, ALTERNATIVES, top_id,
+                              top_logp, saved, work, nbytes)
+            # loss = -sum weight (advantage logp + 0.01 entropy)
+            rs.rs_token_stats_grad(logits, rs.RS_F32, TOKENS, vocab, vocab, target, saved,
+                                   -weight * torch.randn(TOKENS, device=dev), -0.01 * weight, dlogits, vocab)
         rs.rs_router_balance(scores, rs.RS_F32, TOKENS, experts, experts, topk, TOPK, TOPK, None,
                              None, 1, drouter, experts, counts, mean_prob, router_stats, work,
                              nbytes)
-        # backward pass accumulating into the grad DBuffer
-        for i, g in enumerate((dlogits.T @ x, drouter.T @ x, dlogits.sum(0))):
+        # backward pass: through the head and the experts to the hidden states,
+        # the parameters' gradients accumulating into the grad DBuffer
+        dmixed = dlogits @ w
+        rs.rs_expert_combine_grad(dmixed, rs.RS_F32, TOKENS, 512, 512, made, slots, 512, slot, TOPK, gate, TOPK,
+                                  experts, first, taken, drows, 512, dgate, TOPK)
+        live = torch.arange(slots, device=dev) < first[-1]
+        dscales[0].zero_().index_add_(0, of[live], (drows * rows)[live])
+        drows *= scales[0][of]
+        rs.rs_expert_combine(drows, rs.RS_F32, slots, 512, 512, slot, TOKENS, TOPK, None, 0, dmixed, 512, dx, 512)
+        dvalues = gate * (dgate - (gate * dgate).sum(-1, keepdim=True))
+        drouter.scatter_add_(1, topk, dvalues)
+        dx += drouter @ router
+        torch.sum(dx * hidden, 0, out=dscales[1])
+        for i, g in enumerate((dlogits.T @ mixed, drouter.T @ x, dlogits.sum(0))):
             n = specs[i].numel
             grad[plan.pos[i]:plan.pos[i] + n] = g.to(torch.bfloat16).reshape(-1).view(torch.int16)
         rs.rs_group_l2norm_clip(plan.h, rs.RS_ALL, rank, grad, rs.RS_BF16, 1.0, sumsq, clip)
         rs.rs_adam8_step(plan.h, rs.RS_ALL, rank, theta, grad, qm, qv, amax_m, amax_v,
                          lr=1e-3, step=t, grad_scale=clip, bf16_out=gathered)
+        adamw.l2norm_clip(1.0, other_sumsq, other_clip)
+        adamw.step([dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=decay, step=t) for decay in (0.01, 0.0)],
+                   grad_scale=other_clip)
         rs.rs_group_zero(plan.h, rs.RS_ALL, rank, grad, rs.RS_BF16)
         rs.rs_unpack_full(plan.h, rs.RS_ALL, gathered)
     rs.rs_plan_check_device(plan.h)  # no cross-workgroup wait gave up
@@ -103,7 +161,9 @@ def main(steps: int = 3, rank: int = rs.RS_ALL) -> dict:
     out = {"S": plan.S, "padding": plan.padding, "grad_norm": sumsq.sqrt().item(),
            "clip": clip.item(), "weights": [w.view(torch.bfloat16).float() for w in weights],
            "theta": theta, "plan": plan, "preference": pair_stats, "policy": policy_stats,
-           "router": router_stats, "counts": counts}
+           "router": router_stats, "counts": counts,
+           "taken": taken, "entropy": entropy, "top_id": top_id, "top_logp": top_logp, "scales": scales,
+           "scales_norm": other_sumsq.sqrt().item()}
     return out
 
 
