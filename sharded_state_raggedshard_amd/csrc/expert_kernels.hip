@@ -229,7 +229,8 @@ __device__ __forceinline__ void zero_padding(const ExpertRows& a, T* y, int64_t 
     const int lane = lanes::lane();
     const int64_t parts = max(int64_t(1), min(int64_t(64), waves / a.experts));
     for (int64_t q = wave; q < parts * a.experts; q += waves) {
-        const int64_t e = q / parts, used = max(int64_t(0), a.start[e]) + max(0, a.count[e]);
+        // whatever the tables hold, rows of [0, slots) only
+        const int64_t e = q / parts, used = max(int64_t(0), min(a.start[e], a.slots)) + max(0, a.count[e]);
         const int64_t end = min(a.start[e + 1], a.slots);
         for (int64_t r = used + (q - e * parts); r < end; r += parts) {
             T* to = y + r * ldy;

@@ -245,6 +245,22 @@ def test_slots_outside_the_rows_are_not_taken():
     assert not store[:slots].any() and (store[slots:] == 1).all()
 
 
+@pytest.mark.parametrize("first", [(1 << 63) - 1, -(1 << 63), 39, 40])
+def test_padding_of_any_table_stays_inside(first):
+    """Starts and counts that no sort wrote: rows of [0, slots) alone change."""
+    log(f"padding from {first}")
+    slots, hidden = 40, 24
+    store = torch.ones(slots + 8, hidden, device="cuda")
+    start = torch.tensor([first, (1 << 63) - 1], device="cuda")
+    for count in (-(1 << 31), 0, 1, (1 << 31) - 1):
+        store.fill_(1.0)
+        rs.rs_expert_dispatch(store[:1], rs.RS_F32, 0, hidden, hidden, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), 1, None, 0, 1, start,
+                              torch.tensor([count], dtype=torch.int32, device="cuda"), store[4:], slots, hidden)
+        assert (store[:4] == 1).all() and (store[4 + slots:] == 1).all()
+        used = min(max(first, 0), slots) + max(count, 0)
+        assert not store[4 + used:4 + slots].any() and (store[4:4 + min(used, slots)] == 1).all()
+
+
 def test_gradients_against_differences():
     """dispatch -> a row function -> combine, every gradient by central
     differences of the binary64 definition."""
