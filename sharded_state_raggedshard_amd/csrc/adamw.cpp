@@ -135,7 +135,7 @@ rs_status bind(rs_adamw* h, void* const* d_param, const void* const* d_grad, voi
             st = take(spans, d.amax_m, bytes, 4, true);
             if (st == RS_OK) st = take(spans, d.amax_v, bytes, 4, true);
         }
-        if (st == RS_OK && d.out) {
+        if (st == RS_OK && d.out && t.numel > 0) {
             if (t.param != RS_F32) return fail(RS_EINVAL, "a bf16 output beside bf16 parameters");
             st = take(spans, d.out, 2 * t.numel, 2, true);
         }

@@ -476,3 +476,40 @@ def test_root_codes_hold_what_linear_ones_lose():
         h.step([{**hp, "step": t}])
     assert torch.equal(arrays["v"][0], codes)
     h.free()
+
+
+def test_no_elements_at_all():
+    log("adamw without elements")
+    h = rs.AdamW([(0, F32, F32, rs.RS_STATE_F32, 0, 0), (0, BF16, F32, ROOT, 64, 0)]).upload()
+    none = [None, None]
+    h.bind(none, none, none, none, none, none, [None, torch.zeros(4, dtype=torch.bfloat16, device="cuda").data_ptr()])
+    sumsq, scale = torch.ones(1, dtype=torch.float64, device="cuda"), torch.zeros(1, device="cuda")
+    h.l2norm_clip(1.0, sumsq, scale)
+    assert sumsq.item() == 0.0 and scale.item() == 1.0
+    h.step([HP])
+    out = torch.ones(3, device="cuda")
+    h.moments(out, None)
+    assert (out == 1).all()
+    h.free()
+
+
+def test_two_plans_on_two_streams():
+    """Each with its own workspace: what they give does not depend on the other."""
+    log("adamw two plans at once")
+    tensors = [(300_000, F32, BF16, rs.RS_STATE_F32, 0, 0), (5000, F32, BF16, rs.RS_STATE_INT8, 256, 0)]
+    made = [make(tensors, 70, True, out=False) for _ in range(3)]
+    results = [(torch.zeros(1, dtype=torch.float64, device="cuda"), torch.zeros(1, device="cuda")) for _ in made]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for turn in range(5):
+        for (h, _, _), r, s in zip(made, results, [*streams, torch.cuda.current_stream()]):
+            with torch.cuda.stream(s):
+                h.l2norm_clip(1e-2, *r)
+                h.step([HP], grad_scale=r[1])
+    torch.cuda.synchronize()
+    for k in ("params", "m", "v"):
+        for x, y, z in zip(*(m[1][k] for m in made)):
+            assert torch.equal(x, y) and torch.equal(x, z), k
+    assert results[0][0].item() == results[1][0].item() == results[2][0].item()
+    for h, _, _ in made:
+        h.free()
