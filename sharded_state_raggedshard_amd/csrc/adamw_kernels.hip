@@ -10,7 +10,12 @@
 // every wave instruction moves one contiguous span.  Chunks of one tensor are
 // independent: a quantisation block is a power of two up to the chunk, so its
 // absmax never leaves the workgroup.  Every byte is read once and written
-// once, past the caches; what bounds the step is HBM.
+// once, past the caches; what bounds the step is HBM: 218M bf16 weights with
+// binary32 moments 790 us (22 bytes each, 6.1 TB/s), 51.4M binary32 ones with a
+// bf16 copy 222 us behind the norm (28 bytes, 6.5 TB/s), 19.6M with 8-bit
+// moments 38 us (14 bytes, 7.2 TB/s, some of it cached).  Small tensors are
+// bound by the launch and three loads that wait for each other (chunk, tensor,
+// data): 65 vectors of 2048 4.8 us.
 //
 // Arithmetic: the moments follow the blockwise-int8 step's fixed binary32
 // order with no FMA contraction, and the codes come from correctly rounded

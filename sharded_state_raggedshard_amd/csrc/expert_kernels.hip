@@ -2,10 +2,11 @@
 // router's choices by expert, the copy of tokens to their slots, the weighted
 // sum of the slots back to tokens, and its gradient.
 //
-// The sort moves 12 bytes a choice and is bound by its launches.  The others
-// move rows: a token's row is read once for its k slots (dispatch, gradient)
-// or written once from them (combine), a wave or workgroup to a token, so
-// everything is read once and written once; HBM bounds them.
+// The sort moves 12 bytes a choice and is bound by its launches (5 us up to
+// 1024 choices, 11 us up to 131,072).  The others move rows: a token's row is
+// read once for its k slots (dispatch, gradient) or written once from them
+// (combine), a wave or workgroup to a token, so everything is read once and
+// written once; HBM bounds them.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -44,29 +45,32 @@ __device__ __forceinline__ void count_choices(const ExpertSort& a, int64_t c0, i
     }
 }
 
-// Slots of choices [c0, c1) by one wave, in order: the next of expert e is
-// first[e] + next[e].  Lanes of one expert find each other by the bits of its
-// id, and the lowest of them moves next[e] on; a wave's LDS accesses take
-// effect in its order.
+// Slots of 64 consecutive choices, a lane each, by one wave (id: the choice's
+// expert): the next of expert e is first[e] + next[e].  Lanes of one expert
+// find each other by the bits of its id, and the lowest of them moves next[e]
+// on; a wave's LDS accesses take effect in its order.
+__device__ __forceinline__ int place(int id, int experts, int bits, const int* first, int* next) {
+    uint64_t same = ~uint64_t(0);
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (id >> b) & 1;
+        const uint64_t have = __ballot(one);
+        same &= one ? have : ~have;
+    }
+    const int rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
+    if (id >= experts) return -1;
+    const int at = lds_load(&next[id]);
+    if (rank == 0) lds_store(&next[id], at + __popcll(same));
+    return first[id] + at + rank;
+}
+__device__ __forceinline__ int id_bits(int experts) { return 32 - __builtin_clz((unsigned)experts); }
+
+// Slots of choices [c0, c1) by one wave, in order.
 __device__ __forceinline__ void place_choices(const ExpertSort& a, int64_t c0, int64_t c1, const int* first,
                                               int* next) {
-    const int bits = 32 - __builtin_clz((unsigned)a.experts);
+    const int bits = id_bits(a.experts);
     for (int64_t i0 = c0; i0 < c1; i0 += 64) {
         const int64_t i = i0 + lanes::lane();
-        const int id = i < c1 ? choice(a, (uint32_t)i) : a.experts;
-        uint64_t same = ~uint64_t(0);
-        for (int b = 0; b < bits; ++b) {
-            const bool one = (id >> b) & 1;
-            const uint64_t have = __ballot(one);
-            same &= one ? have : ~have;
-        }
-        const int rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
-        int slot = -1;
-        if (id < a.experts) {
-            const int at = lds_load(&next[id]);
-            slot = first[id] + at + rank;
-            if (rank == 0) lds_store(&next[id], at + __popcll(same));
-        }
+        const int slot = place(i < c1 ? choice(a, (uint32_t)i) : a.experts, a.experts, bits, first, next);
         if (i < c1) a.slot[i] = slot;
     }
 }
@@ -92,25 +96,32 @@ __device__ __forceinline__ void first_slots(const ExpertSort& a, int* counts, bo
     }
 }
 
-// All choices in one workgroup of WAVES waves.
+// All choices in one workgroup of WAVES waves, up to kSmallSteps a lane, which
+// are read once.
+constexpr int kSmallSteps = 8;
 template <int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void sort_small_kernel(ExpertSort a) {
     extern __shared__ int lds[];
     constexpr int NT = 64 * WAVES;
     const int tid = threadIdx.x, wave = lanes::wave(), E = a.experts;
-    int* hist = lds;          // per wave
+    int* hist = lds + wave * E;  // of the wave
     int* first = lds + WAVES * E;
-    for (int i = tid; i < WAVES * E; i += NT) hist[i] = 0;
+    const int n = (int)(a.rows * a.k), steps = (n + NT - 1) / NT;
+    const int c0 = wave * steps * 64 + lanes::lane();
+    int id[kSmallSteps];
+#pragma unroll
+    for (int s = 0; s < kSmallSteps; ++s) id[s] = s < steps && c0 + s * 64 < n ? choice(a, c0 + s * 64) : E;
+    for (int i = tid; i < WAVES * E; i += NT) lds[i] = 0;
     __syncthreads();
-    const int64_t n = a.rows * a.k, per = (n + NT - 1) / NT * 64;
-    const int64_t c0 = min(n, wave * per), c1 = min(n, c0 + per);
-    count_choices(a, c0, c1, hist + wave * E);
+#pragma unroll
+    for (int s = 0; s < kSmallSteps; ++s)
+        if (id[s] < E) atomicAdd(&hist[id[s]], 1);
     __syncthreads();
     for (int e = tid; e < E; e += NT) {
         int sum = 0;
         for (int w = 0; w < WAVES; ++w) {
-            const int c = hist[w * E + e];
-            hist[w * E + e] = sum;
+            const int c = lds[w * E + e];
+            lds[w * E + e] = sum;
             sum += c;
         }
         first[e] = sum;
@@ -119,7 +130,13 @@ __global__ __launch_bounds__(64 * WAVES) void sort_small_kernel(ExpertSort a) {
     __syncthreads();
     if (wave == 0) first_slots(a, first, true);
     __syncthreads();
-    place_choices(a, c0, c1, first, hist + wave * E);
+    const int bits = id_bits(E);
+#pragma unroll
+    for (int s = 0; s < kSmallSteps; ++s) {
+        if (s >= steps) break;
+        const int slot = place(id[s], E, bits, first, hist);
+        if (c0 + s * 64 < n) a.slot[c0 + s * 64] = slot;
+    }
 }
 
 // Many choices, first of three launches: chunk c counts its choices.
@@ -258,7 +275,11 @@ __device__ __forceinline__ Share share_of(int pieces, int shares, int i) {
 
 constexpr int kRowThreads = 256;
 
-// A wave takes a share of a token's row and writes it to its k slots.
+// A wave takes a share of a token's row and writes it to its k slots.  Bound by
+// HBM's writes: 16384 x 2880 bf16 to 4 slots 72.5 us (6.5 TB/s), 8192 x 7168 to
+// 8 181 us (5.8 TB/s), and 59 us more for 235 MB of padding rows (segments of
+// 128).  Two pieces a lane: 16384 x 2880 four 76; 2000 x 4096 binary32 to 6
+// 41.5, four 44.
 constexpr int kDispatchPieces = 2;
 template <typename T, bool WEIGHTED, bool LINES>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(ExpertRows a, const T* x, int64_t ldx, T* y, int64_t ldy,
@@ -308,7 +329,9 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(ExpertRows a, con
 }
 
 // A wave takes a share of a token's row from its k slots, B of them in flight.
-// Sums are binary32, in the order of the choices.
+// Sums are binary32, in the order of the choices.  Bound by HBM's reads: 8192 x
+// 7168 bf16 from 8 slots 178 us, 16384 x 2880 from 4 79 us (5.9 TB/s both; four
+// pieces a lane the same).
 constexpr int kCombinePieces = 2;
 template <typename T, bool LINES>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(ExpertRows a, const T* y, int64_t ldy, const T* add,
@@ -379,7 +402,10 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(ExpertRows a, cons
 // slots' rows pass, each giving one dot product and taking w dout.  Rows
 // longer than U NT pieces go in several turns.  A dot product is a lane's
 // binary32 chain of up to U N products a turn, then the lanes' in a fixed
-// order.
+// order.  Bound by HBM: 16384 x 2880 bf16, 4 slots 155 us (5.5 TB/s), 8192 x
+// 7168, 8 slots and 235 MB of padding 433 us (5.2 TB/s).  Rows of y in flight:
+// two of bf16 (four 155 to 158), four of binary32 (2000 x 4096, 6 slots 83 us,
+// two 87).
 constexpr int kGradPieces = 4;
 template <typename T, int NT, bool LINES>
 __global__ __launch_bounds__(NT) void combine_grad_kernel(ExpertRows a, const T* dout, int64_t ldo, const T* y,
@@ -537,12 +563,15 @@ hipError_t combine_grad(const ExpertRows& a, const void* dout, int64_t ldo, cons
 hipError_t launch_expert_sort(const ExpertSort& a, hipStream_t s) {
     const int64_t n = a.rows * a.k;
     const size_t row = size_t(a.experts) * sizeof(int);
-    constexpr int64_t kSmall = 8192;
-    if (n <= kSmall) {
-        if (a.experts <= 512)
-            hipLaunchKernelGGL(sort_small_kernel<16>, dim3(1), dim3(1024), 17 * row, s, a);
-        else
-            hipLaunchKernelGGL(sort_small_kernel<8>, dim3(1), dim3(512), 9 * row, s, a);
+    // One workgroup as long as its lanes hold all choices, three launches after
+    // that (us, one / three: 8192 of 60 experts 9.0 / 10.6, of 256 10.8 / 10.8;
+    // 4096 of 1000, whose counters take eight waves, 11.9 / 14.5).
+    if (n <= 1024 * kSmallSteps && a.experts <= 512) {
+        hipLaunchKernelGGL(sort_small_kernel<16>, dim3(1), dim3(1024), 17 * row, s, a);
+        return hipGetLastError();
+    }
+    if (n <= 512 * kSmallSteps) {
+        hipLaunchKernelGGL(sort_small_kernel<8>, dim3(1), dim3(512), 9 * row, s, a);
         return hipGetLastError();
     }
     const int64_t chunk = sort_chunk(n);
