@@ -19,7 +19,7 @@ struct rs_adamw {
     int64_t total = 0;      // elements of all tensors
     int32_t n_groups = 1;   // highest group + 1
     bool int8 = false;      // some tensor has 8-bit moments
-    size_t off_chunks = 0, off_partial = 0, ws_bytes = 0;
+    size_t off_chunks = 0, off_slots = 0, ws_bytes = 0;
     void* d_ws = nullptr;
     bool uploaded = false, bound = false;
     // the bound arrays and the workspace by their first byte, and the furthest
@@ -202,8 +202,8 @@ rs_status rs_adamw_plan(const rs_adamw_tensor* tensors, int32_t n, rs_adamw** ou
     }
     h->total = total;
     h->off_chunks = align256(size_t(n) * sizeof(rs::aw::Tensor));
-    h->off_partial = h->off_chunks + align256(h->chunks.size() * sizeof(rs::aw::Chunk));
-    h->ws_bytes = h->off_partial + align256(rs::aw::kSumBlocks * sizeof(double));
+    h->off_slots = h->off_chunks + align256(h->chunks.size() * sizeof(rs::aw::Chunk));
+    h->ws_bytes = h->off_slots + align256(rs::aw::kSumWords * sizeof(uint64_t));
     *out = h;
     return RS_OK;
 }
@@ -225,12 +225,14 @@ rs_status rs_adamw_upload(rs_adamw* adamw, void* d_workspace, size_t bytes, void
     if (bytes < adamw->ws_bytes) return fail(RS_ENOMEM, "workspace smaller than rs_adamw_device_bytes()");
     hipStream_t s = as_stream(stream);
     adamw->uploaded = adamw->bound = false;
-    if (!adamw->chunks.empty()) {
-        hipError_t e = hipMemcpyAsync(static_cast<char*>(d_workspace) + adamw->off_chunks, adamw->chunks.data(),
-                                      adamw->chunks.size() * sizeof(rs::aw::Chunk), hipMemcpyHostToDevice, s);
-        if (e == hipSuccess) e = hipStreamSynchronize(s);
-        if (e != hipSuccess) return hip_fail(e, "copying the work table");
-    }
+    static const uint64_t zeros[rs::aw::kSumWords] = {};
+    char* w = static_cast<char*>(d_workspace);
+    hipError_t e = hipMemcpyAsync(w + adamw->off_slots, zeros, sizeof(zeros), hipMemcpyHostToDevice, s);
+    if (e == hipSuccess && !adamw->chunks.empty())
+        e = hipMemcpyAsync(w + adamw->off_chunks, adamw->chunks.data(), adamw->chunks.size() * sizeof(rs::aw::Chunk),
+                           hipMemcpyHostToDevice, s);
+    if (e == hipSuccess) e = hipStreamSynchronize(s);
+    if (e != hipSuccess) return hip_fail(e, "copying the work table");
     adamw->d_ws = d_workspace;
     adamw->uploaded = true;
     return RS_OK;
@@ -259,8 +261,8 @@ rs_status rs_adamw_l2norm_clip(const rs_adamw* adamw, double max_norm, double* d
     if (st == RS_OK) st = check_free(*adamw, d_sumsq, 8);
     if (st == RS_OK) st = check_free(*adamw, d_scale, 4);
     if (st != RS_OK) return st;
-    double* partial = reinterpret_cast<double*>(static_cast<char*>(adamw->d_ws) + adamw->off_partial);
-    hipError_t e = rs::aw::launch_l2norm(work_of(*adamw), partial, d_sumsq, max_norm, d_scale, as_stream(stream));
+    uint64_t* slots = reinterpret_cast<uint64_t*>(static_cast<char*>(adamw->d_ws) + adamw->off_slots);
+    hipError_t e = rs::aw::launch_l2norm(work_of(*adamw), slots, d_sumsq, max_norm, d_scale, as_stream(stream));
     if (e != hipSuccess) return hip_fail(e, "adamw norm launch");
     return RS_OK;
 }

@@ -15,6 +15,8 @@ constexpr int64_t kMaxElems = int64_t(1) << 42;  // of one tensor: chunk indices
 constexpr int32_t kMaxGroups = 16;   // sets of hyper-parameters of one step
 constexpr int kMinBlockLog2 = 6, kMaxBlockLog2 = 12;  // a block lies in one chunk
 constexpr int kSumBlocks = 2048;     // most partial sums of the gradients' norm
+// two words each, then the number of the last call on a line of its own
+constexpr int kSumWords = 2 * kSumBlocks + 32;
 
 // One tensor: where its arrays are and how they are kept.
 struct alignas(16) Tensor {
@@ -53,8 +55,8 @@ struct Scalars {
 };
 
 hipError_t launch_step(const Work& w, const Scalars& sc, const float* gscale, hipStream_t s);
-// partial: kSumBlocks doubles of scratch
-hipError_t launch_l2norm(const Work& w, double* partial, double* sumsq, double max_norm, float* scale,
+// slots: kSumWords words, 0 before the first call
+hipError_t launch_l2norm(const Work& w, uint64_t* slots, double* sumsq, double max_norm, float* scale,
                          hipStream_t s);
 // m, v (nullable): binary32 (f32) or bf16 values of every tensor's moments
 hipError_t launch_moments(const Work& w, void* m, void* v, bool f32, hipStream_t s);
