@@ -10,10 +10,10 @@
 // product gives an exponent.
 //
 // Both kernels are bound by HBM where rows are many: 4096 x 128256 bf16 (1.05
-// GB) take 167 us (6.3 TB/s), with 8 alternatives 183 and with 32 208, and
+// GB) take 169 us (6.2 TB/s), with 8 alternatives 181 and with 32 204, and
 // their gradient 340 us (6.2 TB/s of 2.1 GB); 6001 x 32003 binary32 121 us and
-// 129 with 8.  Few rows are split over workgroups and joined by a second
-// launch: 16 x 128256 9.2 us, with 20 alternatives 14.6.
+// 128 with 8.  Few rows are split over workgroups and joined by a second
+// launch: 16 x 128256 8.9 us, with 20 alternatives 13.4.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -157,6 +157,18 @@ __device__ __forceinline__ float lane_value(float v, int l) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
 }
 
+// before() as one comparison: v in i comes before w in j if order(v, i) >
+// order(w, j).  (-0 counts as 0.)
+__device__ __forceinline__ uint64_t order(float v, int i) {
+    const uint32_t bits = __float_as_uint(v + 0.0f);
+    const uint32_t up = bits ^ (bits & 0x80000000u ? 0xffffffffu : 0x80000000u);
+    return (uint64_t)up << 32 | (uint32_t)~i;
+}
+__device__ __forceinline__ uint64_t lane_key(uint64_t key, int l) {
+    const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(key >> 32), l);
+    return (uint64_t)hi << 32 | (uint32_t)__builtin_amdgcn_readlane((uint32_t)key, l);
+}
+
 // The n-th largest of the wave's 64 values (n <= 64): the least of those that
 // fewer than n are above.
 __device__ __forceinline__ float nth_of_wave(float v, int n) {
@@ -174,14 +186,18 @@ __device__ __forceinline__ void write_best(const float* v, const int32_t* id, in
     if (n <= 64) {
         const float mine = lane < n ? v[lane] : kNegInf;
         const int i = lane < n ? id[lane] : 0x7fffffff;
+        const uint64_t key = order(mine, i);
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += before(lane_value(mine, j), __builtin_amdgcn_readlane(i, j), mine, i) ? 1 : 0;
+        for (int j = 0; j < n; ++j) rank += lane_key(key, j) > key ? 1 : 0;
         if (lane < n && rank < top) write(rank, mine, i);
     } else {
         for (int i = lane; i < n; i += 64) {
+            const float mine = v[i];
+            const int at = id[i];
             int rank = 0;
-            for (int j = 0; j < n; ++j) rank += before(v[j], id[j], v[i], id[i]) ? 1 : 0;
-            if (rank < top) write(rank, v[i], id[i]);
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) rank += before(v[j], id[j], mine, at) ? 1 : 0;
+            if (rank < top) write(rank, mine, at);
         }
     }
     for (int r = n + lane; r < top; r += 64) write(r, kNegInf, -1);
@@ -544,20 +560,32 @@ __global__ __launch_bounds__(64) void stats_join_kernel(TokenStats a) {
     const int64_t first = row * a.parts * a.top + (int64_t)(lane / lanes_each) * a.top;
     const float* v = a.best + first;
     const int32_t* id = a.best_id + first;
-    const float v0 = at0 < a.top ? v[at0] : kNegInf;
+    constexpr int U = 8;
+    float x[U];
+    int32_t xi[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int at = at0 + u * lanes_each;
+        x[u] = kNegInf;
+        xi[u] = -1;
+        if (at < a.top) {
+            x[u] = v[at];
+            xi[u] = id[at];
+        }
+    }
     const PartStat p = a.stat[row * a.parts + lane % a.parts];
     const int64_t y = a.target ? a.target[row] : -1;
     const bool live = !a.target || (y >= 0 && y < a.vocab);
     RowEnd e{};
     if (live) {
         const float top = wave_uniform(lanes::max<64>(p.m));
-        Sums x{kNegInf, p.s, p.w};
-        x.rescale(p.m, top == kNegInf ? 0.0f : top, a.k);
+        Sums all{kNegInf, p.s, p.w};
+        all.rescale(p.m, top == kNegInf ? 0.0f : top, a.k);
         for (int off = 1; off < a.parts; off <<= 1) {
-            x.s += __shfl_xor(x.s, off, 64);
-            x.w += __shfl_xor(x.w, off, 64);
+            all.s += __shfl_xor(all.s, off, 64);
+            all.w += __shfl_xor(all.w, off, 64);
         }
-        e = row_end(x, top, p.token, y >= 0, a.k);
+        e = row_end(all, top, p.token, y >= 0, a.k);
     }
     if (lane == 0) write_row(a, row, live, e);
     if (a.top == 0) return;
@@ -566,18 +594,22 @@ __global__ __launch_bounds__(64) void stats_join_kernel(TokenStats a) {
         return;
     }
     // the n-th largest of the lanes' first values is reached by little more than n
-    const float least = nth_of_wave(v0, a.top);
+    const float least = nth_of_wave(x[0], a.top);
     if (lane == 0) kept = 0;
     __syncthreads();
-    for (int i = at0; i < a.top; i += lanes_each) {
-        const float x = v[i];
-        if (!(x >= least) || x == kNegInf) break;  // they come in order
+    const auto keep = [&](float f, int i) {
+        if (!(f >= least) || f == kNegInf) return false;
         const int at = atomicAdd(&kept, 1);
-        lv[at] = x;
-        li[at] = id[i];
-    }
+        lv[at] = f;
+        li[at] = i;
+        return true;
+    };
+    bool more = true;  // they come in order
+#pragma unroll
+    for (int u = 0; u < U; ++u) more = more && keep(x[u], xi[u]);
+    for (int i = at0 + U * lanes_each; i < a.top && more; i += lanes_each) more = keep(v[i], id[i]);
     __syncthreads();
-    write_best(lv, li, kept, a.top, [&](int rank, float x, int i) { write_top(a, row, rank, x, i, e); });
+    write_best(lv, li, kept, a.top, [&](int rank, float f, int i) { write_top(a, row, rank, f, i, e); });
 }
 
 // ---------------------------------------------------------------- gradient
