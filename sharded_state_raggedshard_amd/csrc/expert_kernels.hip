@@ -81,12 +81,7 @@ __device__ __forceinline__ void first_slots(const ExpertSort& a, int* counts, bo
     const int e0 = lane * per;
     int sum = 0;
     for (int e = e0; e < e0 + per && e < a.experts; ++e) sum += (counts[e] + a.align - 1) / a.align * a.align;
-    int before = sum;
-    for (int off = 1; off < 64; off <<= 1) {
-        const int x = __shfl_up(before, off, 64);
-        if (lane >= off) before += x;
-    }
-    before -= sum;
+    int before = (int)lanes::sum_upto((uint32_t)sum) - sum;
     for (int e = e0; e < e0 + per && e < a.experts; ++e) {
         const int c = (counts[e] + a.align - 1) / a.align * a.align;
         counts[e] = before;
@@ -236,23 +231,52 @@ bool whole_lines(const T* p, int64_t ld) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (int64_t)sizeof(T) % 16 == 0;
 }
 
-// The padding rows of every expert's segment to 0, spread over all waves of
-// the launch (`wave` of `waves`): a wave takes every parts-th padding row of
-// an expert.
-template <typename T>
+// The padding rows of all experts' segments to 0: the r-th of them by wave r of
+// the launch's first kPaddingWaves, then the next ones.  A lane knows an
+// expert's, and the lanes' sums where they begin, so that few experts with many
+// of them keep as many waves busy as many with few (2 rows of 6421 bf16 values,
+// 16 experts' segments of 128: 8.1 us, 33 with a few waves for each expert).
+constexpr int64_t kPaddingWaves = 4096;
+template <bool LINES, typename T>
 __device__ __forceinline__ void zero_padding(const ExpertRows& a, T* y, int64_t ldy, int64_t wave, int64_t waves) {
+    constexpr int GROUPS = 4;  // 64 experts each, in flight together
+    if (wave >= kPaddingWaves) return;
+    waves = min(waves, kPaddingWaves);
     const RowShape<T> shape(a.hidden);
     const u32x4 zero = {0u, 0u, 0u, 0u};
     const int lane = lanes::lane();
-    const int64_t parts = max(int64_t(1), min(int64_t(64), waves / a.experts));
-    for (int64_t q = wave; q < parts * a.experts; q += waves) {
-        // whatever the tables hold, rows of [0, slots) only
-        const int64_t e = q / parts, used = max(int64_t(0), min(a.start[e], a.slots)) + max(0, a.count[e]);
-        const int64_t end = min(a.start[e + 1], a.slots);
-        for (int64_t r = used + (q - e * parts); r < end; r += parts) {
-            T* to = y + r * ldy;
-            for (int p = lane; p < shape.pieces; p += 64) store16(to + p * shape.N, zero);
-            if (lane < shape.tail) to[shape.pieces * shape.N + lane] = T(0);
+    int64_t r = wave, before = 0;
+    for (int e0 = 0; e0 < a.experts; e0 += 64 * GROUPS) {
+        int64_t start[GROUPS], next[GROUPS];
+        int32_t count[GROUPS];
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            const int e = min(e0 + 64 * g + lane, a.experts - 1);
+            start[g] = a.start[e];
+            next[g] = a.start[e + 1];
+            count[g] = a.count[e];
+        }
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            if (e0 + 64 * g >= a.experts) break;
+            // whatever the tables hold, rows of [0, slots) only
+            const int used = (int)min(max(int64_t(0), min(start[g], a.slots)) + max(0, count[g]), a.slots);
+            const int end = (int)max(int64_t(0), min(next[g], a.slots));
+            const uint32_t n = e0 + 64 * g + lane < a.experts && end > used ? (uint32_t)(end - used) : 0u;
+            const uint32_t upto = lanes::sum_upto(n);
+            const uint32_t all = __builtin_amdgcn_readlane(upto, 63);
+            for (; r - before < (int64_t)all; r += waves) {
+                const uint32_t i = (uint32_t)(r - before);
+                const uint64_t later = __ballot(upto > i);
+                if (later == 0) break;  // sums that passed 32 bits
+                const int l = __builtin_ctzll(later);
+                const uint32_t in = i - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(n, l));
+                if (in >= (uint32_t)__builtin_amdgcn_readlane(n, l)) continue;
+                T* to = y + ((int64_t)__builtin_amdgcn_readlane(used, l) + in) * ldy;
+                for (int p = lane; p < shape.pieces; p += 64) put16<LINES>(to + p * shape.N, zero);
+                if (lane < shape.tail) to[shape.pieces * shape.N + lane] = T(0);
+            }
+            before += all;
         }
     }
 }
@@ -325,7 +349,7 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(ExpertRows a, con
             if (tail) to[tail_at] = WEIGHTED ? Vec<T>::pack(Vec<T>::one(one) * w) : one;
         }
     }
-    if (a.start) zero_padding(a, y, ldy, wave0, waves);
+    if (a.start) zero_padding<LINES>(a, y, ldy, wave0, waves);
 }
 
 // A wave takes a share of a token's row from its k slots, B of them in flight.
@@ -398,8 +422,11 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(ExpertRows a, cons
     }
 }
 
-// A workgroup takes a token: its gradient row stays in registers while the k
-// slots' rows pass, each giving one dot product and taking w dout.  Rows
+// A workgroup takes `each` choices of a token: its gradient row stays in
+// registers while their slots' rows pass, each giving one dot product and taking
+// w dout.  All of a token's choices, or what is in flight together where tokens
+// are few (64 x 7168 bf16, 8 slots 7.7 us, all eight 19.5; 600 of them 33.5 and
+// 36.8; but 3001 x 1003 binary32, 6 slots 37.4 and 32.4).  Rows
 // longer than U NT pieces go in several turns.  A dot product is a lane's
 // binary32 chain of up to U N products a turn, then the lanes' in a fixed
 // order.  Bound by HBM: 16384 x 2880 bf16, 4 slots 155 us (5.5 TB/s), 8192 x
@@ -407,15 +434,22 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(ExpertRows a, cons
 // two of bf16 (four 155 to 158), four of binary32 (2000 x 4096, 6 slots 83 us,
 // two 87).
 constexpr int kGradPieces = 4;
+template <typename T>
+constexpr int kGradRows = sizeof(T) == 4 ? 4 : 2;
+constexpr int64_t kFewTokens = 2048;
 template <typename T, int NT, bool LINES>
 __global__ __launch_bounds__(NT) void combine_grad_kernel(ExpertRows a, const T* dout, int64_t ldo, const T* y,
                                                           int64_t ldy, T* dy, int64_t lddy, float* dweight,
-                                                          int64_t lddw) {
-    constexpr int N = Vec<T>::n, U = kGradPieces, WAVES = NT / 64, B = sizeof(T) == 4 ? 4 : 2;
+                                                          int64_t lddw, int each) {
+    constexpr int N = Vec<T>::n, U = kGradPieces, WAVES = NT / 64, B = kGradRows<T>;
     extern __shared__ float red[];  // WAVES x k
     const RowShape<T> shape(a.hidden);
     const int tid = threadIdx.x, wave = lanes::wave();
-    for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
+    const int groups = (a.k + each - 1) / each;
+    const int64_t items = a.rows * groups;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int64_t t = groups == 1 ? item : item / groups;
+        const int first = (int)(item - t * groups) * each, end = min(first + each, a.k);
         const T* from = dout + t * ldo;
         const int32_t* slot = a.slot + t * a.k;
         const int turns = shape.pieces > 0 ? (shape.pieces + U * NT - 1) / (U * NT) : 1;
@@ -430,13 +464,13 @@ __global__ __launch_bounds__(NT) void combine_grad_kernel(ExpertRows a, const T*
             const bool tail = turn == turns - 1 && tid < shape.tail;
             const int tail_at = shape.pieces * N + tid;
             const float vt = tail ? Vec<T>::one(from[tail_at]) : 0.0f;
-            for (int j0 = 0; j0 < a.k; j0 += B) {
+            for (int j0 = first; j0 < end; j0 += B) {
                 u32x4 q[B][U];
                 float qt[B];
                 int at[B];
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
-                    const int j = j0 + b, s = j < a.k ? slot[j] : -1;
+                    const int j = j0 + b, s = j < end ? slot[j] : -1;
                     at[b] = s < a.slots ? s : -1;
                     qt[b] = 0.0f;
                     if (at[b] < 0) continue;
@@ -451,7 +485,7 @@ __global__ __launch_bounds__(NT) void combine_grad_kernel(ExpertRows a, const T*
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
                     const int j = j0 + b;
-                    if (j >= a.k) break;
+                    if (j >= end) break;
                     float dot = 0.0f;
                     if (at[b] >= 0) {
                         const float w = a.weight ? a.weight[t * a.ldw + j] : 1.0f;
@@ -481,21 +515,21 @@ __global__ __launch_bounds__(NT) void combine_grad_kernel(ExpertRows a, const T*
             }
         }
         __syncthreads();
-        for (int j = tid; j < a.k; j += NT) {
+        for (int j = first + tid; j < end; j += NT) {
             float sum = red[j];
             for (int w = 1; w < WAVES; ++w) sum += red[w * a.k + j];
             dweight[t * lddw + j] = sum;
         }
         __syncthreads();
     }
-    if (a.start && dy) zero_padding(a, dy, lddy, blockIdx.x * (int64_t)WAVES + wave, gridDim.x * (int64_t)WAVES);
+    if (a.start && dy) zero_padding<LINES>(a, dy, lddy, blockIdx.x * (int64_t)WAVES + wave, gridDim.x * (int64_t)WAVES);
 }
 
-// Workgroups of a launch over `items` waves' work; enough of them to clear
-// the experts' padding too.
+// Workgroups of `waves` waves over `items` pieces of work; with padding also
+// 2048 waves at least, or one for every slot.
 unsigned row_grid(const ExpertRows& a, int64_t items, int waves, bool padding) {
     int64_t n = (items + waves - 1) / waves;
-    if (padding) n = std::max<int64_t>(n, a.experts);
+    if (padding) n = std::max(n, (std::min<int64_t>(a.slots, 2048) + waves - 1) / waves);
     return grid_of(n);
 }
 
@@ -535,17 +569,20 @@ hipError_t combine(const ExpertRows& a, const void* y, int64_t ldy, const void* 
 template <typename T, int NT>
 hipError_t combine_grad_nt(const ExpertRows& a, const void* dout, int64_t ldo, const void* y, int64_t ldy, void* dy,
                            int64_t lddy, float* dweight, int64_t lddw, hipStream_t s) {
-    const unsigned g = row_grid(a, a.rows, 1, a.start && dy);
+    // a workgroup's waves share a token, but not the padding
+    const int each = a.rows < kFewTokens ? kGradRows<T> : a.k;
+    const int64_t items = a.rows * ((a.k + each - 1) / each);
+    const unsigned g = std::max(row_grid(a, items, 1, false), a.start && dy ? row_grid(a, 0, NT / 64, true) : 0u);
     if (g == 0) return hipSuccess;
     const size_t lds = size_t(NT / 64) * size_t(a.k) * sizeof(float);
     const T *d = static_cast<const T*>(dout), *from = static_cast<const T*>(y);
     T* to = static_cast<T*>(dy);
     if (whole_lines(to, lddy))
         hipLaunchKernelGGL((combine_grad_kernel<T, NT, true>), dim3(g), dim3(NT), lds, s, a, d, ldo, from, ldy, to, lddy,
-                           dweight, lddw);
+                           dweight, lddw, each);
     else
         hipLaunchKernelGGL((combine_grad_kernel<T, NT, false>), dim3(g), dim3(NT), lds, s, a, d, ldo, from, ldy, to, lddy,
-                           dweight, lddw);
+                           dweight, lddw, each);
     return hipGetLastError();
 }
 

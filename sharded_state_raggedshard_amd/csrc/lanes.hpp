@@ -68,6 +68,22 @@ __device__ __forceinline__ double sum64(double v) {
     return swap(v, true);
 }
 
+// Sum of the lanes up to and with this one: within rows of 16, then the last
+// lane of a row to the next one, and lane 31 to the upper half.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_rows(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, ROWS == 0xf);
+}
+__device__ __forceinline__ uint32_t sum_upto(uint32_t v) {
+    v += dpp_rows<0x111, 0xf>(v);  // row_shr: 1, 2, 4, 8, zeros coming in
+    v += dpp_rows<0x112, 0xf>(v);
+    v += dpp_rows<0x114, 0xf>(v);
+    v += dpp_rows<0x118, 0xf>(v);
+    v += dpp_rows<0x142, 0xa>(v);  // row_bcast: 15, to rows 1 and 3
+    v += dpp_rows<0x143, 0xc>(v);  // row_bcast: 31, to rows 2 and 3
+    return v;
+}
+
 // Index of the wave in its workgroup, known to be the same in all lanes.
 __device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
 __device__ __forceinline__ int lane() { return (int)(threadIdx.x & 63); }

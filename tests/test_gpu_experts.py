@@ -221,6 +221,32 @@ def test_combine_grad(shape, dtype, gap):
     assert torch.equal(y[c.real], dy[c.real]) and (ystore[:, c.hidden:] == 77).all()
 
 
+@pytest.mark.parametrize("shape", [(2500, 40, 1000, 6, 8), (2100, 523, 60, 5, 128), (3, 2880, 700, 8, 256)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_many_tokens_and_many_segments(shape, dtype):
+    """More tokens than share workgroups, more experts than are read at once, few tokens with much padding."""
+    log(f"many tokens and segments {shape} {dtype}")
+    c = Case(*shape, dtype, seed=9, gap=0)
+    _, dout = c.array(c.rows)
+    _, y = c.array(c.slots)
+    store, got = c.array(c.slots, fill=3.0)
+    rs.rs_expert_dispatch(dout, dtype, c.rows, c.hidden, c.ld, c.slot, c.k, None, 0, c.experts, c.start, c.count, got, c.slots, c.ld)
+    check_padding(c, store, got, 3.0)
+    assert torch.equal(c.picked(got), torch.where((c.slot >= 0)[..., None], dout.double()[:, None], 0.0))
+    store, dy = c.array(c.slots, fill=3.0)
+    dw = torch.full((c.rows, c.k), 9.0, device="cuda")
+    rs.rs_expert_combine_grad(dout, dtype, c.rows, c.hidden, c.ld, y, c.slots, c.ld, c.slot, c.k, c.weight, c.k + 1, c.experts, c.start,
+                              c.count, dy, c.ld, dw, c.k)
+    check_padding(c, store, dy, 3.0)
+    terms = dout.double()[:, None] * c.picked(y)
+    assert ((dw.double() - terms.sum(-1)).abs() <= 40 * U * terms.abs().sum(-1)).all()
+    # a few of the tokens alone: the same bits
+    some = min(c.rows, 100)
+    dw2 = torch.zeros(some, c.k, device="cuda")
+    rs.rs_expert_combine_grad(dout, dtype, some, c.hidden, c.ld, y, c.slots, c.ld, c.slot, c.k, None, 0, 0, None, None, None, 0, dw2, c.k)
+    assert torch.equal(dw2, dw[:some])
+
+
 def test_slots_outside_the_rows_are_not_taken():
     """A sort of more choices than y has rows for, or a slot map of anything."""
     log("slots out of range")
