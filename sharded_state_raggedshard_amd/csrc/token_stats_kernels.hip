@@ -10,9 +10,9 @@
 // product gives an exponent.
 //
 // Both kernels are bound by HBM where rows are many: 4096 x 128256 bf16 (1.05
-// GB) take 169 us (6.2 TB/s), with 8 alternatives 181 and with 32 204, and
-// their gradient 340 us (6.2 TB/s of 2.1 GB); 6001 x 32003 binary32 121 us and
-// 128 with 8.  Few rows are split over workgroups and joined by a second
+// GB) take 163 us (6.4 TB/s), with 8 alternatives 170 and with 32 194, and
+// their gradient 340 us (6.2 TB/s of 2.1 GB); 6001 x 32003 binary32 119 us and
+// 129 with 8.  Few rows are split over workgroups and joined by a second
 // launch: 16 x 128256 8.9 us, with 20 alternatives 13.4.
 #include <hip/hip_runtime.h>
 
@@ -31,6 +31,7 @@ constexpr double kLn2 = 0.69314718055994530942;
 // Exponents from here on count as this: 2^kLeast is 0, and 0 times it too
 // (a value of -inf has d = -inf).
 constexpr float kLeast = -200.0f;
+constexpr float kNear = 1024.0f;
 
 __device__ __forceinline__ float exponent(float x, float m, float k) { return (x - m) * k; }
 
@@ -58,27 +59,60 @@ struct Sums {
         s *= f;
     }
 
-    template <int C>
-    __device__ __forceinline__ void take(const float (&x)[C], float& ref, float k) {
+    // While values are taken, e and d are of the exponent x k - c, one FMA, for c
+    // = r k rounded, of a reference r with |c| <= kNear: a shift of all of them by
+    // gap = r k - c, which plain() takes out again (2^gap by its series: |gap| <=
+    // 2^-15, the first term left out below 2^-64).  For bf16 the vector unit
+    // would bound rows that HBM brings at its rate: a subtraction and a product
+    // are 64 of some 250 instructions for 32 values.
+    static __device__ __forceinline__ double gap(float r, float k) {
+        const float c = r * k;
+        return fabsf(c) <= kNear ? (double)r * (double)k - (double)c : 0.0;
+    }
+    __device__ __forceinline__ void move(double by) {  // exponents by `by` higher
+        const double l = kLn2 * by, f = 1.0 + l * (1.0 + l * (0.5 + l * (1.0 / 6.0)));
+        w = f * __builtin_fma(by, s, w);
+        s *= f;
+    }
+    __device__ __forceinline__ void plain(float ref, float k) {
+        if (ref != kNegInf) move(-gap(ref, k));
+    }
+
+    template <int C, typename F>
+    __device__ __forceinline__ void add(const float (&x)[C], F exponent_of) {
+        float a[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const float d = exponent_of(x[i]), e = exp2_fast(d);
+            a[i % 4] += e;
+            b[i % 4] = __builtin_fmaf(e, fmaxf(d, kLeast), b[i % 4]);
+        }
+        s += (double)((a[0] + a[1]) + (a[2] + a[3]));
+        w += (double)((b[0] + b[1]) + (b[2] + b[3]));
+    }
+
+    // FAST: by one FMA where it can be; some: values have been taken before.
+    template <bool FAST, int C>
+    __device__ __forceinline__ void take(const float (&x)[C], float& ref, float k, bool some) {
         float v = x[0];
 #pragma unroll
         for (int i = 1; i < C; ++i) v = fmaxf(v, x[i]);
         best = fmaxf(best, v);
         if (__any(exponent(v, ref, k) > 1.0f)) {
             const float to = wave_uniform(lanes::max<64>(fmaxf(ref, v)));
-            rescale(ref, to, k);
+            if (some) {
+                if (FAST) plain(ref, k);
+                rescale(ref, to, k);
+                if (FAST) move(gap(to, k));
+            }
             ref = to;
         }
         const float r = ref == kNegInf ? 0.0f : ref;  // -inf - 0 gives 2^-inf = 0
-        float a[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const float d = exponent(x[i], r, k), e = exp2_fast(d);
-            a[i % 4] += e;
-            b[i % 4] = __builtin_fmaf(e, fmaxf(d, kLeast), b[i % 4]);
-        }
-        s += (double)((a[0] + a[1]) + (a[2] + a[3]));
-        w += (double)((b[0] + b[1]) + (b[2] + b[3]));
+        const float c = wave_uniform(r * k);
+        if (FAST && fabsf(c) <= kNear)
+            add(x, [=](float v) { return __builtin_fmaf(v, k, -c); });
+        else
+            add(x, [=](float v) { return exponent(v, r, k); });
     }
 };
 
@@ -427,13 +461,21 @@ enum { TOP_NONE = 0, TOP_LONG = 1, TOP_HELD = 2 };
 
 // One workgroup per part of a row; its first wave ends the row while the
 // others go on to the next.  256 threads: with 1024 a row's end is too large a
-// share of it (4096 x 128256 bf16 167 us, of 512 176).  Five waves a SIMD, four
-// with the alternatives, is what the registers of 32 values in flight leave
-// without spills.  What the alternatives cost (16 us of 183 with 8) is the
+// share of it.  Four waves a SIMD is what the registers of 32 values and 32 more
+// under way leave without spills (five without alternatives spill: 4096 x 128256
+// bf16 163 us, 200).  What the alternatives cost (8 us of 170 with 8) is the
 // row's end: five barriers, and the stretches read again.
 template <typename T, int NT, int MODE>
-__global__ __launch_bounds__(NT, MODE == TOP_NONE ? 5 : 4) void stats_kernel(TokenStats a) {
+__global__ __launch_bounds__(NT, 4) void stats_kernel(TokenStats a) {
     constexpr bool TOP = MODE != TOP_NONE;
+    // The next take is under way while one is computed, and bf16 exponents are
+    // one FMA each (4096 x 128256 bf16 with 8 alternatives 184 us without both,
+    // 177 with the FMA alone, 188 with the loads alone).  Binary32 has half the
+    // values to compute for a byte, and with alternatives no registers for it
+    // (5000 x 9382 49 us, 57); a part of one take has latency for its bound (16
+    // x 128256 bf16 12.2 us, 12.9).
+    constexpr bool FAST = sizeof(T) == 2 && MODE != TOP_HELD;
+    constexpr bool AHEAD = MODE == TOP_NONE || (MODE == TOP_LONG && sizeof(T) == 2);
     constexpr int N = Vec<T>::n, U = kTake, WAVES = NT / 64;
     __shared__ StatsLds<NT> lds;
     const int tid = threadIdx.x, lane = lanes::lane();
@@ -452,11 +494,16 @@ __global__ __launch_bounds__(NT, MODE == TOP_NONE ? 5 : 4) void stats_kernel(Tok
         const T* base = z + ps.head;
         u32x4 raw[U];
         const auto load = [&](int t) {
+            const int v = part.v0 + tid + t * U * NT;
+            if (AHEAD && part.v0 + (t + 1) * U * NT <= part.v1) {  // all of them, in every thread
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int at = part.v0 + tid + (t * U + u) * NT;
-                raw[u] = Vec<T>::lowest();
-                if (at < part.v1) raw[u] = load16_once(base + at * N);
+                for (int u = 0; u < U; ++u) raw[u] = load16_once(base + (v + u * NT) * N);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    raw[u] = Vec<T>::lowest();
+                    if (v + u * NT < part.v1) raw[u] = load16_once(base + (v + u * NT) * N);
+                }
             }
         };
         load(0);
@@ -475,10 +522,13 @@ __global__ __launch_bounds__(NT, MODE == TOP_NONE ? 5 : 4) void stats_kernel(Tok
         Sums run{kNegInf, 0.0, 0.0};
         float ref = wave_uniform(token), best = kNegInf;
         for (int t = 0, next = seg.per, i = 0; t < seg.takes; ++t) {
-            if (t > 0) load(t);
+            if (!AHEAD && t > 0) load(t);
+            const int there = yv - part.v0 - t * U * NT;
+            if (!AHEAD || (there >= 0 && there < U * NT)) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (part.v0 + tid + (t * U + u) * NT == yv) raw[u] = Vec<T>::lowest();
+                for (int u = 0; u < U; ++u)
+                    if (tid + u * NT == there) raw[u] = Vec<T>::lowest();
+            }
             float x[U * N];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -487,7 +537,8 @@ __global__ __launch_bounds__(NT, MODE == TOP_NONE ? 5 : 4) void stats_kernel(Tok
 #pragma unroll
                 for (int i = 0; i < N; ++i) x[u * N + i] = f[i];
             }
-            run.take(x, ref, k);
+            if (AHEAD && t + 1 < seg.takes) load(t + 1);
+            run.template take<FAST>(x, ref, k, t > 0);
             if (TOP && (t + 1 == next || t + 1 == seg.takes)) {
                 lds.best[i++][tid] = run.best;
                 best = fmaxf(best, run.best);
@@ -495,7 +546,8 @@ __global__ __launch_bounds__(NT, MODE == TOP_NONE ? 5 : 4) void stats_kernel(Tok
                 next += seg.per;
             }
         }
-        if (tid < 64) run.take({one.at == y ? kNegInf : one.value()}, ref, k);
+        if (tid < 64) run.template take<FAST>({one.at == y ? kNegInf : one.value()}, ref, k, true);
+        if (FAST) run.plain(ref, k);
         const double s = lanes::sum64(run.s), w = lanes::sum64(run.w);
         const int wave = tid >> 6;
         turn ^= 1;

@@ -239,6 +239,49 @@ def test_nearly_certain_tokens_keep_their_digits():
         assert ((got["entropy"].double() - h).abs() <= 2 * rel * h + 2.0 ** -126).all()
 
 
+@pytest.mark.parametrize("shift", [0.0, -90.0, 600.0, -1500.0, 2.0 ** 40])
+@pytest.mark.parametrize("rows,vocab,top", [(50, 40_000, 0), (530, 40_000, 0), (530, 40_000, 3), (3, 5000, 3)])
+def test_bf16_rows_far_from_zero(rows, vocab, top, shift):
+    """Rows around any value, the token a lot above the rest or not at all: as the others, and 1 - p keeps its digits."""
+    log(f"token stats {rows} x {vocab} bf16 around {shift}")
+    z, target, g = logits_of(rows, vocab, rs.RS_BF16, 21, width=1.0)
+    z.copy_(z.float() + shift)
+    lift = torch.arange(rows, device="cuda")[:, None] % 60 + 1.0
+    z.scatter_(1, target[:, None], (lift + shift).to(z.dtype))
+    got = run(z, rs.RS_BF16, target, top)
+    check(z, rs.RS_BF16, target, got, 1.0, top)
+    x = Exact(z, target, 1.0)
+    others = torch.where(torch.arange(vocab, device="cuda") == target[:, None], 0.0, torch.exp(x.x)).sum(1)
+    sure = (x.xy[:, 0] == 0) & (others < 1e-3)
+    # three rows are lifted by 3 at most: 5000 e^0.5 / e^3 = 400 of the others' weight
+    assert sure.any() or rows == 3 or abs(shift) > 1e9
+    rel = (3 * x.ax.amax(1) + 20) * U
+    rest = others / (1 + others)
+    assert ((got["saved"][:, 3].double() - rest).abs() <= rel * rest + 2.0 ** -126)[sure].all()
+    assert ((got["logp"].double() + torch.log1p(others)).abs() <= rel * rest + 2.0 ** -126)[sure].all()
+
+
+def test_large_bf16_values():
+    """The ends of the type in rows that are taken in many pieces, ruled out values between them."""
+    log("token stats large bf16 values")
+    for rows, vocab, top in ((6, 40_000, 0), (530, 40_000, 2)):
+        z = torch.zeros(rows, vocab, device="cuda", dtype=torch.bfloat16)
+        z[0], z[1] = 3e38, -3e38
+        z[2, ::2] = -3e38
+        z[2, 1::2] = 3e38
+        z[3, ::2] = -math.inf
+        z[4] = -math.inf
+        z[5, 20_000] = math.inf
+        target = torch.full((rows,), 7, device="cuda")
+        got = run(z, rs.RS_BF16, target, top)
+        want = torch.tensor([math.log(vocab), math.log(vocab), math.log(vocab / 2), math.log(vocab / 2), 0.0], dtype=torch.float64, device="cuda")
+        assert ((got["entropy"][:5].double() - want).abs() <= 20 * U * (1 + want)).all()
+        assert ((got["logp"][:5].double() + want).abs() <= 20 * U * (1 + want)).all()
+        assert torch.isnan(got["entropy"][5]) and torch.isnan(got["logp"][5])
+        if top:
+            assert got["top_id"][:6].tolist() == [[0, 1], [0, 1], [1, 3], [1, 3], [-1, -1], [-1, -1]]
+
+
 def expected_gradient(x, t, live, c, b, temperature):
     """(gradient, tolerance without the output's rounding) in binary64."""
     c, b = c.double()[:, None], b.double()[:, None]
