@@ -23,7 +23,7 @@
  *   - bucket = RS_ALL selects every bucket, rank = RS_ALL every rank.
  *   - stream: a hipStream_t passed as void* (NULL = the null stream).  Every
  *     device call is asynchronous and stream-ordered; nothing synchronises
- *     the host except rs_plan_upload and rs_bind_views.
+ *     the host except the uploads, rs_bind_views and rs_adamw_bind.
  *   - Ownership: the library owns the host-side plans, and a Muon plan also
  *     one stream and two events of its own (created by rs_muon_upload,
  *     released by rs_muon_free).  The caller owns every device allocation
@@ -33,8 +33,9 @@
  *     the host before any launch, and a failed check launches nothing.
  *     rs_last_error() returns a thread-local message for the last non-OK
  *     status of the calling thread.
- *   - Device pointers must be 16-byte aligned (the training objectives state
- *     their own rule).
+ *   - Device pointers must be 16-byte aligned (the training objectives, token
+ *     statistics, tokens to experts and AdamW over many tensors state their
+ *     own rules).
  *   - Concurrency: calls on distinct plans are independent.  Device calls on
  *     one plan share that plan's workspace scratch and must be ordered on
  *     one stream (or synchronised by the caller); the one exception,
