@@ -405,8 +405,9 @@ size_t rs_adamw_device_bytes(const rs_adamw* adamw);
 
 /* Copies the work table into the caller's workspace (>= rs_adamw_device_bytes,
  * 256-byte aligned); the plan keeps the pointer, and what was bound before
- * has to be bound again.  Synchronises the stream.  Errors: RS_EINVAL,
- * RS_ENOMEM (too small), RS_EHIP. */
+ * has to be bound again.  The calls that follow need the device that was
+ * current here (RS_ESTATE on another).  Synchronises the stream.  Errors:
+ * RS_EINVAL, RS_ENOMEM (too small), RS_EHIP. */
 rs_status rs_adamw_upload(rs_adamw* adamw, void* d_workspace, size_t bytes, void* stream);
 
 /* Where the tensors' arrays are: host arrays of n device pointers each, all

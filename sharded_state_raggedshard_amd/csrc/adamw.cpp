@@ -21,6 +21,7 @@ struct rs_adamw {
     bool int8 = false;      // some tensor has 8-bit moments
     size_t off_chunks = 0, off_slots = 0, ws_bytes = 0;
     void* d_ws = nullptr;
+    int device = -1;        // of the workspace
     bool uploaded = false, bound = false;
     // the bound arrays and the workspace by their first byte, and the furthest
     // end of the arrays up to each
@@ -66,10 +67,19 @@ rs::aw::Work work_of(const rs_adamw& h) {
     return k;
 }
 
+// A launch on another device than the workspace's could fault.
+rs_status check_device(const rs_adamw* h) {
+    int device = -1;
+    hipError_t e = hipGetDevice(&device);
+    if (e != hipSuccess) return hip_fail(e, "reading the current device");
+    if (device != h->device) return fail(RS_ESTATE, "adamw plan uploaded on another device than the current one");
+    return RS_OK;
+}
+
 rs_status check_ready(const rs_adamw* h) {
     if (!h->uploaded) return fail(RS_ESTATE, "adamw plan not uploaded");
     if (!h->bound) return fail(RS_ESTATE, "no tensors bound");
-    return RS_OK;
+    return check_device(h);
 }
 
 // An array that a call writes beside the bound ones shares no byte with them.
@@ -155,6 +165,8 @@ rs_status bind(rs_adamw* h, void* const* d_param, const void* const* d_grad, voi
         end.push_back(any);
     }
     if (!h->uploaded) return fail(RS_ESTATE, "adamw plan not uploaded");
+    rs_status at = check_device(h);
+    if (at != RS_OK) return at;
     hipStream_t s = as_stream(stream);
     if (n > 0) {
         hipError_t e = hipMemcpyAsync(h->d_ws, table.data(), n * sizeof(rs::aw::Tensor), hipMemcpyHostToDevice, s);
@@ -227,7 +239,8 @@ rs_status rs_adamw_upload(rs_adamw* adamw, void* d_workspace, size_t bytes, void
     adamw->uploaded = adamw->bound = false;
     static const uint64_t zeros[rs::aw::kSumWords] = {};
     char* w = static_cast<char*>(d_workspace);
-    hipError_t e = hipMemcpyAsync(w + adamw->off_slots, zeros, sizeof(zeros), hipMemcpyHostToDevice, s);
+    hipError_t e = hipGetDevice(&adamw->device);
+    if (e == hipSuccess) e = hipMemcpyAsync(w + adamw->off_slots, zeros, sizeof(zeros), hipMemcpyHostToDevice, s);
     if (e == hipSuccess && !adamw->chunks.empty())
         e = hipMemcpyAsync(w + adamw->off_chunks, adamw->chunks.data(), adamw->chunks.size() * sizeof(rs::aw::Chunk),
                            hipMemcpyHostToDevice, s);
