@@ -355,12 +355,14 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(ExpertRows a, con
 // A wave takes a share of a token's row from its k slots, B of them in flight.
 // Sums are binary32, in the order of the choices.  Bound by HBM's reads: 8192 x
 // 7168 bf16 from 8 slots 178 us, 16384 x 2880 from 4 79 us (5.9 TB/s both; four
-// pieces a lane the same).
+// pieces a lane the same).  bf16 rows of one piece a lane have eight slots in
+// flight (25534 x 264 from 6 30 us, four 36; binary32 has none to gain: 8000 x
+// 250 from 8 19 us, four 15).
 constexpr int kCombinePieces = 2;
-template <typename T, bool LINES>
+template <typename T, int U, bool LINES>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(ExpertRows a, const T* y, int64_t ldy, const T* add,
                                                               int64_t lda, T* out, int64_t ldo, int shares) {
-    constexpr int N = Vec<T>::n, U = kCombinePieces, B = 4, WAVES = kRowThreads / 64;
+    constexpr int N = Vec<T>::n, B = 8 / U, WAVES = kRowThreads / 64;
     const RowShape<T> shape(a.hidden);
     const int lane = lanes::lane();
     const int64_t items = a.rows * shares;
@@ -424,7 +426,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(ExpertRows a, cons
 
 // A workgroup takes `each` choices of a token: its gradient row stays in
 // registers while their slots' rows pass, each giving one dot product and taking
-// w dout.  All of a token's choices, or what is in flight together where tokens
+// w dout.  All of a token's choices, or two (bf16) or four (binary32) where tokens
 // are few (64 x 7168 bf16, 8 slots 7.7 us, all eight 19.5; 600 of them 33.5 and
 // 36.8; but 3001 x 1003 binary32, 6 slots 37.4 and 32.4).  Rows
 // longer than U NT pieces go in several turns.  A dot product is a lane's
@@ -432,16 +434,17 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(ExpertRows a, cons
 // order.  Bound by HBM: 16384 x 2880 bf16, 4 slots 155 us (5.5 TB/s), 8192 x
 // 7168, 8 slots and 235 MB of padding 433 us (5.2 TB/s).  Rows of y in flight:
 // two of bf16 (four 155 to 158), four of binary32 (2000 x 4096, 6 slots 83 us,
-// two 87).
+// two 87), eight where a row is one piece a lane (25534 x 264 bf16, 6 slots 72
+// us, two 80; 8000 x 250 binary32, 8 slots 34, four 41).
 constexpr int kGradPieces = 4;
-template <typename T>
-constexpr int kGradRows = sizeof(T) == 4 ? 4 : 2;
+template <typename T, int U>
+constexpr int kGradRows = U == 1 ? 8 : sizeof(T) == 4 ? 4 : 2;
 constexpr int64_t kFewTokens = 2048;
-template <typename T, int NT, bool LINES>
+template <typename T, int NT, int U, bool LINES>
 __global__ __launch_bounds__(NT) void combine_grad_kernel(ExpertRows a, const T* dout, int64_t ldo, const T* y,
                                                           int64_t ldy, T* dy, int64_t lddy, float* dweight,
                                                           int64_t lddw, int each) {
-    constexpr int N = Vec<T>::n, U = kGradPieces, WAVES = NT / 64, B = kGradRows<T>;
+    constexpr int N = Vec<T>::n, WAVES = NT / 64, B = kGradRows<T, U>;
     extern __shared__ float red[];  // WAVES x k
     const RowShape<T> shape(a.hidden);
     const int tid = threadIdx.x, wave = lanes::wave();
@@ -510,10 +513,15 @@ __global__ __launch_bounds__(NT) void combine_grad_kernel(ExpertRows a, const T*
                         if (dy && tail) to[tail_at] = Vec<T>::pack(vt * w);
                         dot = lanes::sum<64>(lo + hi);
                     }
-                    if (lanes::lane() == 0) red[wave * a.k + j] = turn == 0 ? dot : red[wave * a.k + j] + dot;
+                    if (lanes::lane() != 0) continue;
+                    if (WAVES == 1)  // rows of one turn
+                        dweight[t * lddw + j] = dot;
+                    else
+                        red[wave * a.k + j] = turn == 0 ? dot : red[wave * a.k + j] + dot;
                 }
             }
         }
+        if (WAVES == 1) continue;
         __syncthreads();
         for (int j = first + tid; j < end; j += NT) {
             float sum = red[j];
@@ -551,26 +559,34 @@ hipError_t dispatch(const ExpertRows& a, const void* x, int64_t ldx, void* y, in
                     : dispatch_weighted<T, false>(a, static_cast<const T*>(x), ldx, static_cast<T*>(y), ldy, s);
 }
 
-template <typename T>
-hipError_t combine(const ExpertRows& a, const void* y, int64_t ldy, const void* add, int64_t lda, void* out,
-                   int64_t ldo, hipStream_t s) {
-    const int shares = shares_of<kCombinePieces>((int)(a.hidden / Vec<T>::n));
+template <typename T, int U>
+hipError_t combine_pieces(const ExpertRows& a, const T* y, int64_t ldy, const T* add, int64_t lda, T* out,
+                          int64_t ldo, hipStream_t s) {
+    const int shares = shares_of<U>((int)(a.hidden / Vec<T>::n));
     const unsigned g = row_grid(a, a.rows * shares, kRowThreads / 64, false);
     if (g == 0) return hipSuccess;
-    const T *from = static_cast<const T*>(y), *more = static_cast<const T*>(add);
-    T* to = static_cast<T*>(out);
-    if (whole_lines(to, ldo))
-        hipLaunchKernelGGL((combine_kernel<T, true>), dim3(g), dim3(kRowThreads), 0, s, a, from, ldy, more, lda, to, ldo, shares);
+    if (whole_lines(out, ldo))
+        hipLaunchKernelGGL((combine_kernel<T, U, true>), dim3(g), dim3(kRowThreads), 0, s, a, y, ldy, add, lda, out, ldo, shares);
     else
-        hipLaunchKernelGGL((combine_kernel<T, false>), dim3(g), dim3(kRowThreads), 0, s, a, from, ldy, more, lda, to, ldo, shares);
+        hipLaunchKernelGGL((combine_kernel<T, U, false>), dim3(g), dim3(kRowThreads), 0, s, a, y, ldy, add, lda, out, ldo, shares);
     return hipGetLastError();
 }
 
-template <typename T, int NT>
+template <typename T>
+hipError_t combine(const ExpertRows& a, const void* y, int64_t ldy, const void* add, int64_t lda, void* out,
+                   int64_t ldo, hipStream_t s) {
+    const T *from = static_cast<const T*>(y), *more = static_cast<const T*>(add);
+    T* to = static_cast<T*>(out);
+    if constexpr (sizeof(T) == 2)
+        if (a.hidden / Vec<T>::n <= 64) return combine_pieces<T, 1>(a, from, ldy, more, lda, to, ldo, s);
+    return combine_pieces<T, kCombinePieces>(a, from, ldy, more, lda, to, ldo, s);
+}
+
+template <typename T, int NT, int U>
 hipError_t combine_grad_nt(const ExpertRows& a, const void* dout, int64_t ldo, const void* y, int64_t ldy, void* dy,
                            int64_t lddy, float* dweight, int64_t lddw, hipStream_t s) {
     // a workgroup's waves share a token, but not the padding
-    const int each = a.rows < kFewTokens ? kGradRows<T> : a.k;
+    const int each = a.rows < kFewTokens ? kGradRows<T, kGradPieces> : a.k;
     const int64_t items = a.rows * ((a.k + each - 1) / each);
     const unsigned g = std::max(row_grid(a, items, 1, false), a.start && dy ? row_grid(a, 0, NT / 64, true) : 0u);
     if (g == 0) return hipSuccess;
@@ -578,10 +594,10 @@ hipError_t combine_grad_nt(const ExpertRows& a, const void* dout, int64_t ldo, c
     const T *d = static_cast<const T*>(dout), *from = static_cast<const T*>(y);
     T* to = static_cast<T*>(dy);
     if (whole_lines(to, lddy))
-        hipLaunchKernelGGL((combine_grad_kernel<T, NT, true>), dim3(g), dim3(NT), lds, s, a, d, ldo, from, ldy, to, lddy,
+        hipLaunchKernelGGL((combine_grad_kernel<T, NT, U, true>), dim3(g), dim3(NT), lds, s, a, d, ldo, from, ldy, to, lddy,
                            dweight, lddw, each);
     else
-        hipLaunchKernelGGL((combine_grad_kernel<T, NT, false>), dim3(g), dim3(NT), lds, s, a, d, ldo, from, ldy, to, lddy,
+        hipLaunchKernelGGL((combine_grad_kernel<T, NT, U, false>), dim3(g), dim3(NT), lds, s, a, d, ldo, from, ldy, to, lddy,
                            dweight, lddw, each);
     return hipGetLastError();
 }
@@ -590,9 +606,11 @@ template <typename T>
 hipError_t combine_grad(const ExpertRows& a, const void* dout, int64_t ldo, const void* y, int64_t ldy, void* dy,
                         int64_t lddy, float* dweight, int64_t lddw, hipStream_t s) {
     const int64_t pieces = a.hidden / Vec<T>::n;
-    if (pieces <= 64 * kGradPieces) return combine_grad_nt<T, 64>(a, dout, ldo, y, ldy, dy, lddy, dweight, lddw, s);
-    if (pieces <= 128 * kGradPieces) return combine_grad_nt<T, 128>(a, dout, ldo, y, ldy, dy, lddy, dweight, lddw, s);
-    return combine_grad_nt<T, 256>(a, dout, ldo, y, ldy, dy, lddy, dweight, lddw, s);
+    constexpr int U = kGradPieces;
+    if (pieces <= 64) return combine_grad_nt<T, 64, 1>(a, dout, ldo, y, ldy, dy, lddy, dweight, lddw, s);
+    if (pieces <= 64 * U) return combine_grad_nt<T, 64, U>(a, dout, ldo, y, ldy, dy, lddy, dweight, lddw, s);
+    if (pieces <= 128 * U) return combine_grad_nt<T, 128, U>(a, dout, ldo, y, ldy, dy, lddy, dweight, lddw, s);
+    return combine_grad_nt<T, 256, U>(a, dout, ldo, y, ldy, dy, lddy, dweight, lddw, s);
 }
 
 }  // namespace
