@@ -793,25 +793,28 @@ class AdamW:
         return self
 
     def bind(self, params, grads, m, v, amax_m=None, amax_v=None, bf16_out=None, stream=None):
-        """Tensors are checked against the plan's sizes and types."""
+        """Tensors are checked against the plan's sizes and types (bf16 may also
+        be its bits in int16 or uint16); addresses are taken as they are."""
+        import torch
         n = len(self.tensors)
         lists = [params, grads, m, v, amax_m, amax_v, bf16_out]
         if any(x is not None and len(x) != n for x in lists):
             raise RaggedShardError(RS_EINVAL, f"{n} entries per list needed")
-        sizes = {RS_F32: 4, RS_BF16: 2}
+        f32, bf16 = (torch.float32,), (torch.bfloat16, torch.int16, torch.uint16)
+        types = {RS_F32: f32, RS_BF16: bf16}
         for i, (numel, p, g, state, block, _) in enumerate(self.tensors):
             eight = state != RS_STATE_F32
             blocks = -(-numel // block) if eight else 0
-            each = ((params, numel, sizes[p]), (grads, numel, sizes[g]), (m, numel, 1 if eight else 4),
-                    (v, numel, 1 if eight else 4), (amax_m, blocks, 4), (amax_v, blocks, 4),
-                    (bf16_out, numel, 2))
-            for x, count, size in each:
+            each = ((params, numel, types[p]), (grads, numel, types[g]), (m, numel, (torch.int8,) if eight else f32),
+                    (v, numel, (torch.uint8,) if eight else f32), (amax_m, blocks, f32), (amax_v, blocks, f32),
+                    (bf16_out, numel, bf16))
+            for x, count, dtypes in each:
                 x = None if x is None else x[i]
                 if x is None or isinstance(x, int) or (count == 0 and x is not params[i]):
                     continue
-                if x.numel() != count or x.element_size() != size or not x.is_contiguous():
-                    raise RaggedShardError(RS_EINVAL, f"tensor {i}: not {count} contiguous elements "
-                                                      f"of {size} bytes")
+                if x.numel() != count or not x.is_contiguous() or (count > 0 and x.dtype not in dtypes):
+                    raise RaggedShardError(RS_EINVAL, f"tensor {i}: {x.numel()} elements of {x.dtype}, not {count} "
+                                                      f"contiguous ones of {dtypes[0]}")
         rs_adamw_bind(self.h, *lists, stream=stream)
         self.arrays = lists
         return self

@@ -1,0 +1,57 @@
+"""The AdamW class of the binding: what it refuses before the library is
+called, on tensors of the host (a call that gets past its checks is refused for
+the device that they are on)."""
+import pytest
+import torch
+
+import sharded_state_raggedshard_amd as rs
+
+F32, BF16 = rs.RS_F32, rs.RS_BF16
+N, BLOCK = 600, 256
+
+
+def lists(**other):
+    """Arrays of a binary32 tensor with 8-bit moments and of a bf16 one with binary32 moments."""
+    a = dict(params=[torch.zeros(N), torch.zeros(N, dtype=torch.bfloat16)],
+             grads=[torch.zeros(N, dtype=torch.bfloat16), torch.zeros(N)],
+             m=[torch.zeros(N, dtype=torch.int8), torch.zeros(N)], v=[torch.zeros(N, dtype=torch.uint8), torch.zeros(N)],
+             amax_m=[torch.zeros(3), None], amax_v=[torch.zeros(3), None],
+             bf16_out=[torch.zeros(N, dtype=torch.bfloat16), None])
+    for name, (i, dtype) in other.items():
+        a[name][i] = a[name][i].to(dtype)
+    return a
+
+
+@pytest.fixture
+def adamw():
+    h = rs.AdamW([(N, F32, BF16, rs.RS_STATE_INT8, BLOCK, 0), (N, BF16, F32, rs.RS_STATE_F32, 0, 0)])
+    yield h
+    h.free()
+
+
+@pytest.mark.parametrize("other", [{}, dict(grads=(0, torch.int16), bf16_out=(0, torch.uint16)), dict(params=(1, torch.int16))])
+def test_types_of_the_plan_pass(adamw, other):
+    """bf16 also as its bits."""
+    with pytest.raises(rs.RaggedShardError, match="not on the current device"):
+        adamw.bind(**lists(**other))
+
+
+WRONG = [("params", 0, torch.int32), ("params", 1, torch.float16), ("grads", 0, torch.float16), ("grads", 1, torch.int32),
+         ("m", 0, torch.uint8), ("v", 0, torch.int8), ("m", 1, torch.int32), ("v", 1, torch.int32), ("amax_m", 0, torch.int32),
+         ("amax_v", 0, torch.int32), ("bf16_out", 0, torch.float16)]
+
+
+@pytest.mark.parametrize("name,i,dtype", WRONG)
+def test_other_types_of_the_same_width_are_refused(adamw, name, i, dtype):
+    with pytest.raises(rs.RaggedShardError, match=f"tensor {i}: .*{dtype}") as e:
+        adamw.bind(**lists(**{name: (i, dtype)}))
+    assert e.value.status == rs.RS_EINVAL
+    assert adamw.arrays is None
+
+
+def test_an_empty_tensor_of_another_type_is_not_looked_at():
+    h = rs.AdamW([(0, F32, F32, rs.RS_STATE_F32, 0, 0), (N, F32, F32, rs.RS_STATE_F32, 0, 0)])
+    empty, full = torch.zeros(0, dtype=torch.float16), torch.zeros(N)
+    with pytest.raises(rs.RaggedShardError, match="not on the current device"):
+        h.bind(*[[empty, full] for _ in range(4)])
+    h.free()
