@@ -788,8 +788,10 @@ class AdamW:
     def upload(self, device="cuda", stream=None):
         import torch
         nbytes = rs_adamw_device_bytes(self.h)
-        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        rs_adamw_upload(self.h, self.workspace, nbytes, stream)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        rs_adamw_upload(self.h, workspace, nbytes, stream)
+        # only now: a refused call leaves the plan in the old one
+        self.workspace, self.arrays = workspace, None
         return self
 
     def bind(self, params, grads, m, v, amax_m=None, amax_v=None, bf16_out=None, stream=None):

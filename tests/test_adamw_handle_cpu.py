@@ -55,3 +55,19 @@ def test_an_empty_tensor_of_another_type_is_not_looked_at():
     with pytest.raises(rs.RaggedShardError, match="not on the current device"):
         h.bind(*[[empty, full] for _ in range(4)])
     h.free()
+
+
+def test_a_refused_upload_leaves_what_was_there(adamw):
+    """The plan still points into the old workspace, so somebody has to hold it."""
+    workspace, arrays = object(), [object()]
+    adamw.workspace, adamw.arrays = workspace, arrays
+    with pytest.raises(rs.RaggedShardError, match="not on the current device"):
+        adamw.upload(device="cpu")
+    assert adamw.workspace is workspace and adamw.arrays is arrays
+
+
+def test_an_upload_lets_go_of_what_was_bound(adamw, monkeypatch):
+    monkeypatch.setattr(rs, "rs_adamw_upload", lambda *a: None)
+    adamw.arrays = [object()]
+    assert adamw.upload(device="cpu") is adamw
+    assert adamw.workspace.numel() == rs.rs_adamw_device_bytes(adamw.h) and adamw.arrays is None
