@@ -818,7 +818,7 @@ class AdamW:
                     raise RaggedShardError(RS_EINVAL, f"tensor {i}: {x.numel()} elements of {x.dtype}, not {count} "
                                                       f"contiguous ones of {dtypes[0]}")
         rs_adamw_bind(self.h, *lists, stream=stream)
-        self.arrays = lists
+        self.arrays = [None if x is None else list(x) for x in lists]
         return self
 
     def l2norm_clip(self, max_norm: float, sumsq, scale=None, stream=None):

@@ -71,3 +71,17 @@ def test_an_upload_lets_go_of_what_was_bound(adamw, monkeypatch):
     adamw.arrays = [object()]
     assert adamw.upload(device="cpu") is adamw
     assert adamw.workspace.numel() == rs.rs_adamw_device_bytes(adamw.h) and adamw.arrays is None
+
+
+def test_what_is_bound_does_not_follow_the_callers_lists(adamw, monkeypatch):
+    """The plan points to the tensors that were bound: they live on when the
+    caller's lists let go of them, as where gradients are set to None."""
+    monkeypatch.setattr(rs, "rs_adamw_bind", lambda *a, **k: None)
+    a = lists()
+    bound = [list(x) for x in a.values()]
+    adamw.bind(**a)
+    for x in a.values():
+        x[0] = None
+        x.clear()
+    assert all(held is not None and len(held) == len(was) and all(x is y for x, y in zip(held, was))
+               for held, was in zip(adamw.arrays, bound))

@@ -35,7 +35,7 @@ def test_a_refused_upload_leaves_a_working_plan():
 def test_a_refused_binding_writes_nothing_and_keeps_the_old_one():
     log("adamw refused binding")
     h, a = made()
-    other = {k: [x[0].clone().half() if k == "params" else x[0].clone()] for k, x in a.items()}
+    other = {k: [x[0].clone().int() if k == "params" else x[0].clone()] for k, x in a.items()}
     with pytest.raises(rs.RaggedShardError):
         h.bind(**other)
     h.step([HP])
