@@ -427,8 +427,11 @@ rs_status rs_adamw_bind(rs_adamw* adamw, void* const* d_param, const void* const
  * fixed order (NaN / Inf propagate); with d_scale (nullable) the clipping
  * coefficient for max_norm, as rs_clip_coef.  (Where other gradients count in
  * the norm, add the sums and call rs_clip_coef.)  Uses the workspace: calls
- * on one plan must be ordered.  Errors: RS_EINVAL (max_norm not finite and
- * > 0 with d_scale; an output among the bound arrays), RS_ESTATE, RS_EHIP. */
+ * on one plan must be ordered.  A call whose bounded wait for its own partial
+ * sums gave up, which only overlapping calls can bring about, gives NaN, and
+ * so does every later one until the next rs_adamw_upload.  Errors: RS_EINVAL
+ * (max_norm not finite and > 0 with d_scale; an output among the bound
+ * arrays), RS_ESTATE, RS_EHIP. */
 rs_status rs_adamw_l2norm_clip(const rs_adamw* adamw, double max_norm, double* d_sumsq,
                                float* d_scale, void* stream);
 

@@ -409,7 +409,10 @@ __device__ __forceinline__ double sumsq_chunk(const Tensor& t, int64_t pos, int 
 // cleared in between.  Relaxed device-scope accesses pass the XCDs' L2 caches
 // by; an ordered one would write them back.  The wait is for workgroups that
 // wait for nobody, and bounded all the same: a call that gives up, as only
-// overlapping calls on one workspace could, returns NaN.
+// overlapping calls on one workspace could, returns NaN and leaves a mark.  A
+// workgroup of it that starts after its end takes the number that it left for
+// the last call's, and its slot would pass for the next call's: so behind a
+// mark every call returns NaN, until the next upload clears the words.
 //
 // What the memory-side cache keeps of the gradients is there for the step that
 // follows: norm and step of 51.4M parameters 241 us instead of 254.
@@ -427,8 +430,12 @@ __global__ __launch_bounds__(NT) void sumsq_kernel(const Tensor* __restrict__ te
     __shared__ double lds[NT / 64];
     __shared__ uint32_t call;
     const int tid = threadIdx.x;
-    uint64_t* number = slots + 2 * kSumBlocks;
-    if (tid == 0) call = (uint32_t)slot_load(number) + 1u;
+    uint64_t *number = slots + 2 * kSumBlocks, *mark = number + 1;
+    bool marked = false;
+    if (tid == 0) {
+        call = (uint32_t)slot_load(number) + 1u;
+        if (blockIdx.x == gridDim.x - 1) marked = slot_load(mark) != 0;
+    }
     double sum = 0.0;
     for (int64_t c = blockIdx.x; c < n_chunks; c += gridDim.x) {
         const Chunk ch = chunks[c];
@@ -457,13 +464,14 @@ __global__ __launch_bounds__(NT) void sumsq_kernel(const Tensor* __restrict__ te
             if (lo >> 32 == call && hi >> 32 == call) break;
             if (++spins > kSpinLimit) {
                 lost = true;
+                slot_store(mark, 1);
                 break;
             }
             __builtin_amdgcn_s_sleep(1);
         }
         total += __builtin_bit_cast(double, (hi << 32) | (uint32_t)lo);
     }
-    total = wg_sum<NT>(lost ? __builtin_nan("") : total, lds);
+    total = wg_sum<NT>(lost || marked ? __builtin_nan("") : total, lds);
     if (tid != 0) return;
     *sumsq = total;
     if (scale) {
