@@ -15,8 +15,8 @@ constexpr int64_t kMaxElems = int64_t(1) << 42;  // of one tensor: chunk indices
 constexpr int32_t kMaxGroups = 16;   // sets of hyper-parameters of one step
 constexpr int kMinBlockLog2 = 6, kMaxBlockLog2 = 12;  // a block lies in one chunk
 constexpr int kSumBlocks = 2048;     // most partial sums of the gradients' norm
-// Two words each, then on a line of their own the number of the last call and
-// a mark that one of them gave up.
+// Two words each, then on a line of its own the number of the last call (low
+// half) and a mark that one of them gave up (high half).
 constexpr int kSumWords = 2 * kSumBlocks + 32;
 
 // One tensor: where its arrays are and how they are kept.

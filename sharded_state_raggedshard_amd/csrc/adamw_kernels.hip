@@ -409,10 +409,11 @@ __device__ __forceinline__ double sumsq_chunk(const Tensor& t, int64_t pos, int 
 // cleared in between.  Relaxed device-scope accesses pass the XCDs' L2 caches
 // by; an ordered one would write them back.  The wait is for workgroups that
 // wait for nobody, and bounded all the same: a call that gives up, as only
-// overlapping calls on one workspace could, returns NaN and leaves a mark.  A
-// workgroup of it that starts after its end takes the number that it left for
-// the last call's, and its slot would pass for the next call's: so behind a
-// mark every call returns NaN, until the next upload clears the words.
+// overlapping calls on one workspace could, returns NaN and leaves a mark
+// beside the number.  A workgroup of it that starts after its end takes the
+// number that it left for the last call's, and its slot would pass for the next
+// call's: so behind a mark every call returns NaN, until the next upload clears
+// both.  (One load brings both: a second one cost 1.3 us.)
 //
 // What the memory-side cache keeps of the gradients is there for the step that
 // follows: norm and step of 51.4M parameters 241 us instead of 254.
@@ -423,6 +424,9 @@ __device__ __forceinline__ uint64_t slot_load(const uint64_t* p) {
 __device__ __forceinline__ void slot_store(uint64_t* p, uint64_t v) {
     __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+__device__ __forceinline__ void half_store(uint32_t* p, uint32_t v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 
 __global__ __launch_bounds__(NT) void sumsq_kernel(const Tensor* __restrict__ tensors,
                                                  const Chunk* __restrict__ chunks, int64_t n_chunks,
@@ -430,11 +434,13 @@ __global__ __launch_bounds__(NT) void sumsq_kernel(const Tensor* __restrict__ te
     __shared__ double lds[NT / 64];
     __shared__ uint32_t call;
     const int tid = threadIdx.x;
-    uint64_t *number = slots + 2 * kSumBlocks, *mark = number + 1;
+    uint64_t* last = slots + 2 * kSumBlocks;
+    uint32_t *number = reinterpret_cast<uint32_t*>(last), *mark = number + 1;
     bool marked = false;
     if (tid == 0) {
-        call = (uint32_t)slot_load(number) + 1u;
-        if (blockIdx.x == gridDim.x - 1) marked = slot_load(mark) != 0;
+        const uint64_t both = slot_load(last);
+        call = (uint32_t)both + 1u;
+        marked = both >> 32 != 0;
     }
     double sum = 0.0;
     for (int64_t c = blockIdx.x; c < n_chunks; c += gridDim.x) {
@@ -464,7 +470,7 @@ __global__ __launch_bounds__(NT) void sumsq_kernel(const Tensor* __restrict__ te
             if (lo >> 32 == call && hi >> 32 == call) break;
             if (++spins > kSpinLimit) {
                 lost = true;
-                slot_store(mark, 1);
+                half_store(mark, 1);
                 break;
             }
             __builtin_amdgcn_s_sleep(1);
@@ -478,7 +484,7 @@ __global__ __launch_bounds__(NT) void sumsq_kernel(const Tensor* __restrict__ te
         const double c = max_norm / (sqrt(total) + 1e-6);
         *scale = (float)(c < 1.0 ? c : total == total ? 1.0 : total);
     }
-    slot_store(number, call);
+    half_store(number, call);
 }
 
 // ----------------------------------------------------- moments as values

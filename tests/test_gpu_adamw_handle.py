@@ -44,14 +44,14 @@ def test_a_refused_binding_writes_nothing_and_keeps_the_old_one():
 
 
 def test_a_norm_that_gave_up_shows_until_the_next_upload():
-    """The mark that a bounded wait leaves, set from the host: the last 32 words
+    """The mark that a bounded wait leaves, set from the host: the last 64 words
     of the workspace begin with the number of the last call, then the mark."""
     log("adamw norm behind a mark")
     h, a = made(3 * 4096 + 5)
     sumsq, scale = torch.zeros(1, dtype=torch.float64, device="cuda"), torch.zeros(1, device="cuda")
     n = a["grads"][0].numel()
     for turn in range(2):
-        words = h.workspace.view(torch.int64)[-32:]
+        words = h.workspace.view(torch.int32)[-64:]
         for call in (1, 2):
             h.l2norm_clip(1.0, sumsq, scale)
             assert sumsq.item() == n and abs(scale.item() * n ** 0.5 - 1) < 1e-5
