@@ -165,10 +165,16 @@ __device__ __forceinline__ float level_v(uint32_t code, bool root) {
 // New parameters of four elements from their new moments: the hardware square
 // root and reciprocal (one ulp each, the update then within 8 ulp), or
 // correctly rounded operations where an update beyond 0.02, infinite or NaN
-// could leave 1e-8 + 1e-6 |theta| with them.
+// could leave 1e-8 + 1e-6 |theta| with them.  The hardware counts a subnormal v
+// as 0, and a reciprocal below 2^-126: the first shows beside an eps that is
+// not far above 2^-63 kappa, the second with one beyond 2^100.
 __device__ __forceinline__ void new_params(const StepScalars& sc, const float (&th)[4], const float* m,
                                            const float* v, float (&t)[4]) {
-    bool exact = false;
+    bool exact = !(sc.eps <= 0x1p100f);
+    if (__builtin_expect(!(sc.kappa * 0x1p-39f <= sc.eps), 0)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) exact = exact || (v[j] > 0.0f && v[j] < 0x1p-126f);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float den = (__builtin_amdgcn_sqrtf(v[j]) * sc.kappa) + sc.eps;
