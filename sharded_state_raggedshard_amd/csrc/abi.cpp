@@ -539,6 +539,7 @@ rs_status adam8_step(const rs_plan* plan, int32_t bucket, int32_t rank, float* d
     sc.c_decay = (float)(1.0 - hp->lr * hp->weight_decay);
     sc.step_size = (float)(hp->lr / (1.0 - std::pow(hp->beta1, t)));
     sc.kappa = (float)(1.0 / std::sqrt(1.0 - std::pow(hp->beta2, t)));
+    sc.limit = rs::update_limit(sc.kappa, sc.eps);
     rs::StepBuffers b;
     b.theta = d_master;
     b.grad = d_grad;

@@ -122,14 +122,15 @@ __device__ __forceinline__ float param(const StepScalars& sc, float theta, float
 // within 1 ulp): the update u then carries a relative error below 8 ulp
 // (4.8e-7) against the correctly rounded evaluation, so for |u| <= 0.02 the
 // new parameter differs by at most 9.6e-9 plus one rounding of the result,
-// inside |d| <= 1e-8 + 1e-6 |theta|.  Any other u (larger, infinite or NaN)
-// sets `exact` and the caller recomputes with correctly rounded operations.
+// inside |d| <= 1e-8 + 1e-6 |theta|.  Any other u (beyond the step's limit,
+// which an unusual eps makes every one, infinite or NaN) sets `exact` and the
+// caller recomputes with correctly rounded operations.
 // No quantisation code depends on the parameter.
 __device__ __forceinline__ float param_fast(const StepScalars& sc, float theta, float m, float v,
                                             bool& exact) {
     const float den = (__builtin_amdgcn_sqrtf(v) * sc.kappa) + sc.eps;
     const float u = sc.step_size * (m * __builtin_amdgcn_rcpf(den));
-    exact = exact || !(fabsf(u) <= 0.02f);
+    exact = exact || !(fabsf(u) <= sc.limit);
     return (theta * sc.c_decay) - u;
 }
 

@@ -304,6 +304,7 @@ rs_status rs_adamw_step(const rs_adamw* adamw, const rs_adam_hparams* hp, int32_
         s.c_decay = (float)(1.0 - p.lr * p.weight_decay);
         s.step_size = (float)(p.lr / (1.0 - std::pow(p.beta1, t)));
         s.kappa = (float)(1.0 / std::sqrt(1.0 - std::pow(p.beta2, t)));
+        s.limit = rs::update_limit(s.kappa, s.eps);
     }
     rs_status st = check_ready(adamw);
     if (st == RS_OK) st = check_free(*adamw, d_grad_scale, 4);

@@ -165,21 +165,15 @@ __device__ __forceinline__ float level_v(uint32_t code, bool root) {
 // New parameters of four elements from their new moments: the hardware square
 // root and reciprocal (one ulp each, the update then within 8 ulp), or
 // correctly rounded operations where an update beyond 0.02, infinite or NaN
-// could leave 1e-8 + 1e-6 |theta| with them.  The hardware counts a subnormal v
-// as 0, and a reciprocal below 2^-126: the first shows beside an eps that is
-// not far above 2^-63 kappa, the second with one beyond 2^100.
+// could leave 1e-8 + 1e-6 |theta| with them, or an unusual eps asks for them.
 __device__ __forceinline__ void new_params(const StepScalars& sc, const float (&th)[4], const float* m,
                                            const float* v, float (&t)[4]) {
-    bool exact = !(sc.eps <= 0x1p100f);
-    if (__builtin_expect(!(sc.kappa * 0x1p-39f <= sc.eps), 0)) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) exact = exact || (v[j] > 0.0f && v[j] < 0x1p-126f);
-    }
+    bool exact = false;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float den = (__builtin_amdgcn_sqrtf(v[j]) * sc.kappa) + sc.eps;
         const float u = sc.step_size * (m[j] * __builtin_amdgcn_rcpf(den));
-        exact = exact || !(fabsf(u) <= 0.02f);
+        exact = exact || !(fabsf(u) <= sc.limit);
         t[j] = (th[j] * sc.c_decay) - u;
     }
     if (__builtin_expect(exact, 0)) {

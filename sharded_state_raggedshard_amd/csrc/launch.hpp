@@ -60,7 +60,18 @@ hipError_t l2_scratch(double** out, int64_t* capacity);
 // fp32 step scalars derived on the host.
 struct StepScalars {
     float beta1, beta2, omega1, omega2, eps, c_decay, step_size, kappa;
+    float limit;  // largest update that the hardware's root and reciprocal give
 };
+
+// With them (one ulp each) an update is within 8 ulp, 2^-21 of itself, which is
+// 1e-8 at 0.02.  But the hardware counts a subnormal v as 0: with its root,
+// below 2^-63, goes up to 2^-63 kappa / eps of the update, where the other
+// roundings take 2^-22.  And it counts a reciprocal below 2^-126 as 0, which an
+// eps beyond 2^100 can have.  Then every update takes correctly rounded
+// operations.
+inline float update_limit(float kappa, float eps) {
+    return kappa * 0x1p-41f <= eps && eps <= 0x1p100f ? 0.02f : -1.0f;
+}
 
 struct StepBuffers {
     float* theta;

@@ -9,6 +9,7 @@ import torch
 
 import sharded_state_raggedshard_amd as rs
 from gpu_harness import log
+from synth import ROWS, TensorSpec
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +57,33 @@ def test_against_binary64(eps, top_v, top_m, state):
     assert ((params.double() - want).abs() <= tol).all()
     assert top_v != 1e-38 or (v1 < 2.0 ** -126).any()
     h.free()
+
+
+@pytest.mark.parametrize("eps,top_v,top_m", [(1e-30, 1e-38, 1e-30), (1e-16, 1e-38, 1e-16), (1e-8, 1e-36, 1e-8), (3e38, 1e30, 1e38)])
+def test_the_planned_step_against_binary64(eps, top_v, top_m):
+    """Blocks of 256 as rows of a planned tensor; tolerances as above."""
+    log(f"planned step eps {eps}")
+    rows, block = 41, 256
+    n = rows * block
+    plan = rs.Plan([TensorSpec("w", (rows, block), ROWS, 1)], 1, 16).upload()
+    g = torch.Generator(device="cuda").manual_seed(6)
+    am = torch.full((rows,), top_m, device="cuda")
+    av = (top_v * 10.0 ** (-5 * torch.rand(rows, device="cuda", generator=g, dtype=torch.float64))).float()
+    qm, qv = torch.zeros(plan.total, dtype=torch.int8, device="cuda"), torch.zeros(plan.total, dtype=torch.uint8, device="cuda")
+    here = slice(plan.pos[0], plan.pos[0] + n)
+    qm[here] = torch.randint(-127, 128, (n,), device="cuda", generator=g).to(torch.int8)
+    qv[here] = torch.randint(200, 256, (n,), device="cuda", generator=g).to(torch.uint8)
+    params = torch.zeros(plan.total, device="cuda")
+    spread = lambda x: x.double().repeat_interleave(block)  # noqa: E731
+    m1 = 0.9 * (qm[here].double() / 127 * spread(am))
+    v1 = 0.999 * (qv[here].double() / 255 * spread(av))
+    size, kappa = 1e-3 / (1 - 0.9 ** 400), 1 / math.sqrt(1 - 0.999 ** 400)
+    den = v1.sqrt() * kappa + float(torch.tensor(eps, dtype=torch.float32))
+    want = -size * m1 / den
+    off_v = (10 * U * v1 + 4 * 2.0 ** -150) / (2 * v1.sqrt()) * kappa / den
+    off_m = (7 * U * m1.abs() + 3 * 2.0 ** -150) / den
+    rs.rs_adam8_step(plan.h, rs.RS_ALL, rs.RS_ALL, params, torch.zeros(plan.total, dtype=torch.int16, device="cuda"), qm, qv, am, av,
+                     lr=1e-3, beta1=0.9, beta2=0.999, eps=eps, weight_decay=0.0, step=400)
+    tol = 1e-8 + 1e-6 * want.abs() + want.abs() * off_v + size * off_m
+    assert ((params[here].double() - want).abs() <= tol).all()
+    plan.free()
