@@ -702,8 +702,10 @@ rs_status rs_router_balance(const void* d_logits, int32_t dtype, int64_t rows, i
  * -- what a sampler reports, and what a loss of the caller's own is made of --
  * and the logits' gradient from the gradients of the first two.  Rows, strides,
  * dtypes, tokens and rows that take no part as at the training objectives.
- * Exponents take log2(e) / temperature rounded to binary32 (a temperature off
- * by up to 2^-24 of itself); exponentials are binary32, sums as there. */
+ * Exponents take log2(e) / temperature rounded to binary32, a temperature off
+ * by up to 2^-24 of itself: log-probabilities are corrected for it, entropies
+ * and gradients keep it (an entropy is off by up to 2^-24 of the variance of
+ * log p); exponentials are binary32, sums as there. */
 
 /* Scratch bytes of rs_token_stats (they serve every smaller size); 0 for sizes
  * it refuses. */

@@ -27,7 +27,8 @@ Scratch scratch_of(int64_t rows, int32_t top) {
     return s;
 }
 
-float exponent_scale(double temperature) { return (float)(1.44269504088896340736 / temperature); }
+constexpr double kLog2e = 1.44269504088896340736;
+float exponent_scale(double temperature) { return (float)(kLog2e / temperature); }
 
 // What both calls take.
 rs_status check_common(const void* z, int32_t dtype, int64_t rows, int64_t vocab, int64_t ld, const int64_t* target,
@@ -85,6 +86,8 @@ rs_status rs_token_stats(const void* d_logits, int32_t dtype, int64_t rows, int6
     a.ld = ld;
     a.target = d_target;
     a.k = exponent_scale(temperature);
+    a.scale = 1.0 / temperature;
+    a.skew = kLog2e * a.scale / (double)a.k - 1.0;
     a.top = top;
     a.logp = d_logp;
     a.entropy = d_entropy;

@@ -25,6 +25,7 @@ struct TokenStats {
     int64_t rows, vocab, ld;
     const int64_t* target;  // nullable: rows have no token, and all take part
     float k;                // log2(e) / temperature
+    double scale, skew;     // 1 / temperature; log2(e) scale / k - 1
     int32_t top;
     float* logp;     // nullable
     float* entropy;  // nullable

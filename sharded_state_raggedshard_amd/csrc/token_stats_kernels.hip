@@ -5,9 +5,13 @@
 // With m the row's maximum, d_i = (z_i - m) k, k = log2(e) / T in binary32,
 // e_i = 2^d_i, S = sum e and W = sum e d:
 //   log p_i = ln 2 d_i - ln S,   H = -sum p log p = ln S - ln 2 W / S.
-// Every quantity takes the same rounded k, a temperature off by up to 2^-24 of
-// itself, which moves a log-probability by 2^-24 (|log p| + H); so one
-// product gives an exponent.
+// One product gives an exponent, with the rounded k: a temperature off by s = up
+// to 2^-24 of itself.  What that does to ln S is known at the row's end to first
+// order, s E[(z - m) / T] (the second is s^2 / 2 of the exponents' variance), and
+// the value's own (z - m) / T is taken in binary64: so log-probabilities are
+// free of it.  The entropy keeps it, 2^-24 of that variance, and the gradient,
+// whose p_i are then off by 2^-24 (|log p_i| + H) of themselves, like a rounding
+// of their exponents.
 //
 // Both kernels are bound by HBM where rows are many: 4096 x 128256 bf16 (1.05
 // GB) take 163 us (6.4 TB/s), with 8 alternatives 170 and with 32 194, and
@@ -142,14 +146,14 @@ __device__ __forceinline__ RowEnd row_end(const Sums& x, float ref, float token,
 }
 
 // log p of value v
-__device__ __forceinline__ double log_p(const RowEnd& e, float v, float k) {
-    return ((double)v - (double)e.m) * ((double)k * kLn2) - e.ln_s;
+__device__ __forceinline__ double log_p(const TokenStats& a, const RowEnd& e, float v) {
+    return ((double)v - (double)e.m) * a.scale - (e.ln_s - a.skew * e.down);
 }
 
 // The outputs of a row but its alternatives, by one thread.
 __device__ __forceinline__ void write_row(const TokenStats& a, int64_t row, bool live, const RowEnd& e) {
     const bool none = !live || e.empty;
-    if (a.logp) a.logp[row] = none ? 0.0f : (float)log_p(e, e.token, a.k);
+    if (a.logp) a.logp[row] = none ? 0.0f : (float)log_p(a, e, e.token);
     if (a.entropy) a.entropy[row] = none ? 0.0f : (float)(e.ln_s + e.down);
     if (a.saved) {
         float* to = a.saved + 4 * row;
@@ -165,7 +169,7 @@ __device__ __forceinline__ void write_row(const TokenStats& a, int64_t row, bool
 __device__ __forceinline__ void write_top(const TokenStats& a, int64_t row, int rank, float v, int id, const RowEnd& e) {
     const bool bad = e.S != e.S;
     a.top_id[row * a.top + rank] = bad || id < 0 ? -1 : id;
-    a.top_logp[row * a.top + rank] = bad ? __builtin_nanf("") : id < 0 ? kNegInf : (float)log_p(e, v, a.k);
+    a.top_logp[row * a.top + rank] = bad ? __builtin_nanf("") : id < 0 ? kNegInf : (float)log_p(a, e, v);
 }
 
 // Candidates for the alternatives of a part of a row: the best n of them come
