@@ -73,3 +73,40 @@ def test_any_temperature_keeps_the_last_digit(rows, vocab, dtype):
         rs.rs_token_logp(z, dtype, rows, vocab, vocab, target, other, torch.zeros(nb, dtype=torch.uint8, device="cuda"), nb,
                          temperature=temperature)
         assert ((other - logp).abs() <= torch.nextafter(logp.abs(), torch.tensor(math.inf, device="cuda")) - logp.abs()).all(), temperature
+
+
+@pytest.mark.parametrize("rows,vocab", SHAPES)
+@pytest.mark.parametrize("dtype", [rs.RS_F32, rs.RS_BF16])
+@pytest.mark.parametrize("token", ["none", "another"])
+def test_nearly_certain_rows_keep_their_digits_whatever_their_token(rows, vocab, dtype, token):
+    """A value 9 to 24 above the rest that is not the row's token: what the
+    others weigh, most of it in its neighbours (a thread's same 32 values), is
+    known to (3 |x| + 20) U of itself and 2^-51 of 1 + rest, a sum in binary64;
+    so are -log p of the value and the entropy, which is rest (1 + mean |x|)."""
+    log(f"token stats certain rows {rows} x {vocab} {dtype} token {token}")
+    g = torch.Generator(device="cuda").manual_seed(vocab + 1)
+    for shift in (0.0, -90.0, 33.0):
+        a = 9 + 15 * torch.rand(rows, 3, device="cuda", generator=g)
+        z = torch.full((rows, vocab), shift - 70, device="cuda") + torch.randn(rows, vocab, device="cuda", generator=g)
+        at = (torch.rand(rows, 1, device="cuda", generator=g) * (vocab // 4 - 1)).long() * 4 + 1
+        z.scatter_(1, at, shift + 10.0)
+        for i, near in enumerate((-1, 1, 2)):
+            z.scatter_(1, at + near, shift + 10.0 - a[:, i:i + 1])
+        z = z.to(TYPE[dtype])
+        target = None if token == "none" else (at[:, 0] + vocab // 2) % vocab
+        x = z.double() - z.double().gather(1, at)
+        others = torch.exp(x).scatter(1, at, 0.0)
+        rest = others.sum(1)
+        assert (rest < 1e-3).all() and (rest > 0).all()
+        want, h = -torch.log1p(rest), torch.log1p(rest) - (others * x).sum(1) / (1 + rest)
+        rel = (3 * 90 + 20) * U
+        logp, entropy, top_id, top_logp = run(z, dtype, target, 2, 1.0)
+        assert torch.equal(top_id[:, 0], at[:, 0])
+        assert (top_logp <= 0).all() and (entropy >= 0).all()
+        assert ((top_logp[:, 0].double() - want).abs() <= rel * rest + 2.0 ** -51).all()
+        assert ((entropy.double() - h).abs() <= 2 * rel * h + 2.0 ** -51).all()
+        if target is not None:
+            own = x.gather(1, target[:, None])[:, 0] + want
+            assert ((logp.double() - own).abs() <= U * own.abs() + rel * rest).all()
+        # without alternatives the same sums
+        assert ((run(z, dtype, target, 0, 1.0)[1].double() - h).abs() <= 2 * rel * h + 2.0 ** -51).all()
