@@ -705,9 +705,10 @@ rs_status rs_router_balance(const void* d_logits, int32_t dtype, int64_t rows, i
  * Exponents take log2(e) / temperature rounded to binary32, a temperature off
  * by up to 2^-24 of itself: log-probabilities are corrected for it, entropies
  * and gradients keep it (an entropy is off by up to 2^-24 of the variance of
- * log p); exponentials are binary32, sums as there, and a value that is nearly
- * the whole row stands apart from them like the token, whether it is the token
- * or not.  No log-probability is above 0, no entropy below. */
+ * log p); exponentials are binary32, sums as there, and a value beside which
+ * all others have less than 2^-10 of its probability stands apart from them
+ * like the token, whether it is the token or not.  No log-probability is above
+ * 0, no entropy below. */
 
 /* Scratch bytes of rs_token_stats (they serve every smaller size); 0 for sizes
  * it refuses. */

@@ -36,8 +36,10 @@ constexpr double kLn2 = 0.69314718055994530942;
 // (a value of -inf has d = -inf).
 constexpr float kLeast = -200.0f;
 constexpr float kNear = 1024.0f;
-// Sums around their largest value that are nearly all of it.
-constexpr double kSure = 1.0625;
+// A value whose exponent lies this far above the others' may be nearly the whole
+// row: 2^-10 of it and less is known to its own last digits, more to 2^-22 as all
+// sums of 32 values are.
+constexpr float kFar = 10.0f;
 
 __device__ __forceinline__ float exponent(float x, float m, float k) { return (x - m) * k; }
 
@@ -99,26 +101,25 @@ struct Sums {
 
     // A new reference is itself one of the values.  Where it is nearly the whole
     // row, a binary32 sum with it would round away the rest that the entropy and
-    // its own log-probability are made of: so values of its size join s here,
-    // exactly 1 each as their exponent is 0, and x goes on without them.  (+inf
-    // stays, for a NaN.)
+    // its own log-probability are made of: then the wave's values of its size join
+    // s here, exactly 1 each as their exponent is 0, and x goes on without them.
+    // It can be only if no other lane's largest value comes near it; doing so for
+    // every new reference cost rows of one take 11%.
     template <int C>
     __device__ __forceinline__ void apart(float (&x)[C], float ref) {
-        const float top = ref < __builtin_inff() ? ref : __builtin_nanf("");
         int n = 0;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const bool is = x[i] == top;
-            n += is ? 1 : 0;
+            const bool is = x[i] == ref;
+            n += __popcll(__ballot(is));
             x[i] = is ? kNegInf : x[i];
         }
-        s += (double)n;
+        s += (double)(lanes::lane() == 0 ? n : 0);
     }
 
-    // FAST: by one FMA where it can be; some: values have been taken before; sure:
-    // a new reference may be nearly the whole row.
+    // FAST: by one FMA where it can be; some: values have been taken before.
     template <bool FAST, int C>
-    __device__ __forceinline__ void take(float (&x)[C], float& ref, float k, bool some, bool sure) {
+    __device__ __forceinline__ void take(float (&x)[C], float& ref, float k, bool some) {
         float v = x[0];
 #pragma unroll
         for (int i = 1; i < C; ++i) v = fmaxf(v, x[i]);
@@ -130,7 +131,8 @@ struct Sums {
                 rescale(ref, to, k);
             }
             ref = to;
-            if (sure) apart(x, to);
+            // (of +inf none does: its difference is a NaN, and shall be the sum's)
+            if (__popcll(__ballot(exponent(v, to, k) > -kFar)) == 1) apart(x, to);
             if (FAST) move(gap(to, k));
         }
         const float r = ref == kNegInf ? 0.0f : ref;  // -inf - 0 gives 2^-inf = 0
@@ -494,10 +496,11 @@ enum { TOP_NONE = 0, TOP_LONG = 1, TOP_HELD = 2 };
 // others go on to the next.  256 threads: with 1024 a row's end is too large a
 // share of it.  Four waves a SIMD is what the registers of 32 values and 32 more
 // under way leave without spills (five without alternatives spill: 4096 x 128256
-// bf16 163 us, 200).  What the alternatives cost (8 us of 170 with 8) is the
+// bf16 163 us, 200); binary32 with alternatives is held to five (5000 x 9382 46
+// us, 52 with four).  What the alternatives cost (8 us of 170 with 8) is the
 // row's end: five barriers, and the stretches read again.
 template <typename T, int NT, int MODE>
-__global__ __launch_bounds__(NT, 4) void stats_kernel(TokenStats a) {
+__global__ __launch_bounds__(NT, sizeof(T) == 4 && MODE == TOP_LONG ? 5 : 4) void stats_kernel(TokenStats a) {
     constexpr bool TOP = MODE != TOP_NONE;
     // The next take is under way while one is computed, and bf16 exponents are
     // one FMA each (4096 x 128256 bf16 with 8 alternatives 184 us without both,
@@ -550,52 +553,39 @@ __global__ __launch_bounds__(NT, 4) void stats_kernel(TokenStats a) {
         const float token = y >= 0 ? Vec<T>::one(z[y]) : kNegInf;
         const Single<T> one(z, ps, part, y);
         const int yv = ps.piece(y);
-        // A part of one take, still in registers, finds out at its end whether a
-        // reference of its own is nearly all of a wave's share, and only then is
-        // taken again with it apart (16 x 128256 bf16 with 20 alternatives 12.9 us,
-        // 13.2 with it apart in every row).
-        const float first = wave_uniform(token);
-        Sums run;
-        float ref, best;
-        double s, w;
-        for (bool sure = MODE != TOP_HELD;; sure = true) {
-            run = Sums{kNegInf, 0.0, 0.0};
-            ref = first;
-            best = kNegInf;
-            for (int t = 0, next = seg.per, i = 0; t < seg.takes; ++t) {
-                if (!AHEAD && t > 0) load(t);
-                const int there = yv - part.v0 - t * U * NT;
-                if (!AHEAD || (there >= 0 && there < U * NT)) {
+        Sums run{kNegInf, 0.0, 0.0};
+        float ref = wave_uniform(token), best = kNegInf;
+        for (int t = 0, next = seg.per, i = 0; t < seg.takes; ++t) {
+            if (!AHEAD && t > 0) load(t);
+            const int there = yv - part.v0 - t * U * NT;
+            if (!AHEAD || (there >= 0 && there < U * NT)) {
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
-                        if (tid + u * NT == there) raw[u] = Vec<T>::lowest();
-                }
-                float x[U * N];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float f[N];
-                    Vec<T>::open(raw[u], f);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) x[u * N + i] = f[i];
-                }
-                if (AHEAD && t + 1 < seg.takes) load(t + 1);
-                run.template take<FAST>(x, ref, k, t > 0, sure);
-                if (TOP && (t + 1 == next || t + 1 == seg.takes)) {
-                    lds.best[i++][tid] = run.best;
-                    best = fmaxf(best, run.best);
-                    run.best = kNegInf;
-                    next += seg.per;
-                }
+                for (int u = 0; u < U; ++u)
+                    if (tid + u * NT == there) raw[u] = Vec<T>::lowest();
             }
-            if (tid < 64) {
-                float x[1] = {one.at == y ? kNegInf : one.value()};
-                run.template take<FAST>(x, ref, k, true, true);
+            float x[U * N];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float f[N];
+                Vec<T>::open(raw[u], f);
+#pragma unroll
+                for (int i = 0; i < N; ++i) x[u * N + i] = f[i];
             }
-            if (FAST) run.plain(ref, k);
-            s = lanes::sum64(run.s);
-            w = lanes::sum64(run.w);
-            if (sure || ref == first || !(s < kSure)) break;
+            if (AHEAD && t + 1 < seg.takes) load(t + 1);
+            run.template take<FAST>(x, ref, k, t > 0);
+            if (TOP && (t + 1 == next || t + 1 == seg.takes)) {
+                lds.best[i++][tid] = run.best;
+                best = fmaxf(best, run.best);
+                run.best = kNegInf;
+                next += seg.per;
+            }
         }
+        if (tid < 64) {
+            float x[1] = {one.at == y ? kNegInf : one.value()};
+            run.template take<FAST>(x, ref, k, true);
+        }
+        if (FAST) run.plain(ref, k);
+        const double s = lanes::sum64(run.s), w = lanes::sum64(run.w);
         const int wave = tid >> 6;
         turn ^= 1;
         if (lane == 0) {
