@@ -216,16 +216,30 @@ struct Candidates {
             id[at] = i;
         }
     }
+    // The same, but of more than kRoom of them a fair choice is left (each takes a
+    // place of those before it at random, and keeps it if there is one), in which
+    // v and id need not match.
+    __device__ __forceinline__ void sample(float x, int i) {
+        const uint32_t before = (uint32_t)atomicAdd(&n, 1);
+        const uint32_t at = before < kRoom ? before : __umulhi((uint32_t)i * 2654435761u, before + 1);
+        if (at < kRoom) {
+            v[at] = x;
+            id[at] = i;
+        }
+    }
+    __device__ __forceinline__ bool full() const {
+        return __hip_atomic_load(&n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) > kRoom;
+    }
 };
-
-__device__ __forceinline__ bool before(float v, int i, float w, int j) { return v > w || (v == w && i < j); }
 
 __device__ __forceinline__ float lane_value(float v, int l) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
 }
 
-// before() as one comparison: v in i comes before w in j if order(v, i) >
-// order(w, j).  (-0 counts as 0.)
+// By value and then by index, as one comparison: v in i comes before w in j if
+// order(v, i) > order(w, j).  (-0 counts as 0.  Two comparisons in a row, of the
+// value and then of the index, wait for each other's loads: 160 us for a row of
+// ties in 16 parts, 49 so.)
 __device__ __forceinline__ uint64_t order(float v, int i) {
     const uint32_t bits = __float_as_uint(v + 0.0f);
     const uint32_t up = bits ^ (bits & 0x80000000u ? 0xffffffffu : 0x80000000u);
@@ -261,9 +275,10 @@ __device__ __forceinline__ void write_best(const float* v, const int32_t* id, in
         for (int i = lane; i < n; i += 64) {
             const float mine = v[i];
             const int at = id[i];
+            const uint64_t key = order(mine, at);
             int rank = 0;
 #pragma unroll 8
-            for (int j = 0; j < n; ++j) rank += before(v[j], id[j], mine, at) ? 1 : 0;
+            for (int j = 0; j < n; ++j) rank += order(v[j], id[j]) > key ? 1 : 0;
             if (rank < top) write(rank, mine, at);
         }
     }
@@ -322,7 +337,7 @@ struct Segments {
 // among what reaches it: about n to 2 n values, in as many threads' stretches,
 // which the workgroup reads again (from a cache, if the first read went
 // through it).  lds.c.n passes kRoom where that many tie with it or a few
-// stretches hold them.  Begins behind the barrier that lds.group is written
+// stretches hold them; then the rest is not looked at.  Begins behind the barrier that lds.group is written
 // before; ends with one.
 // HELD: a part is one take, still in registers.
 template <typename T, int NT, bool HELD>
@@ -362,7 +377,8 @@ __device__ __forceinline__ void gather_best(const T* z, const Pieces<T>& ps, con
     const int length = seg.per * kTake, shift = length > 1 ? 32 - __builtin_clz((unsigned)(length - 1)) : 0;
     const int all = lds.n_hot << shift, yv = ps.piece(y);
     const T* base = z + ps.head;
-    for (int q0 = tid; q0 < all; q0 += B * NT) {
+#pragma unroll 1
+    for (int q0 = tid; q0 < all && !lds.c.full(); q0 += B * NT) {
         u32x4 raw[B];
         int at[B];
 #pragma unroll
@@ -390,62 +406,52 @@ __device__ __forceinline__ void gather_best(const T* z, const Pieces<T>& ps, con
     __syncthreads();
 }
 
-// The same for a part whose candidates did not fit: rounds over the part, each
-// taking the next smaller value and how often it is there, until n are found;
-// then what lies above the last one, and of its equals the first by index.
+// The same for a part whose candidates did not fit: what lies above the bound
+// alone, and as far as n are missing then, its equals by index.  That is little
+// in a row masked with the type's lowest value.  Where it does not fit either,
+// the n-th largest of a sample is a higher bound that n values reach, and about
+// n / kRoom of them lie above it: rows of 128256 with 7 values beside the lowest
+// and 8 alternatives 383 us for 4096 of them (170 with -inf in their place; the
+// next smaller value found pass by pass took 2284).
 template <typename T, int NT>
 __device__ void gather_slow(const T* z, const Pieces<T>& ps, const Part& part, int n, StatsLds<NT>& lds) {
     constexpr int N = Vec<T>::n;
     const int tid = threadIdx.x;
     const T* base = z + ps.head;
     const int edges = part.ends ? ps.edges : 0;
-    float last = -kNegInf;
-    int above = 0;
-    for (int found = 0; found < n;) {
-        float top = kNegInf;
-        int count = 0;
-        const auto see = [&](float x) {
-            if (!(x < last) || x < top || x == kNegInf) return;
-            count = x > top ? 1 : count + 1;
-            top = x;
-        };
+    float last = lds.least;
+    int above;
+    for (;;) {
+        __syncthreads();  // every thread has seen what is overwritten now
+        if (tid == 0) lds.c.n = 0;
+        __syncthreads();
         for (int v = part.v0 + tid; v < part.v1; v += NT) {
             float x[N];
             Vec<T>::open(load16(base + v * N), x);
-            for (int i = 0; i < N; ++i) see(x[i]);
+            for (int i = 0; i < N; ++i)
+                if (x[i] > last) lds.c.sample(x[i], ps.head + v * N + i);
         }
-        if (tid < edges) see(Vec<T>::one(z[ps.edge(tid)]));
-        const float most = lanes::max<64>(top);
-        if (lanes::lane() == 0) lds.red[tid >> 6] = most;
-        if (tid == 0) lds.n_hot = 0;
+        if (tid < edges) {
+            const float x = Vec<T>::one(z[ps.edge(tid)]);
+            if (x > last) lds.c.sample(x, ps.edge(tid));
+        }
+        __syncthreads();
+        above = lds.c.n;
+        __syncthreads();
+        if (above <= kRoom) break;
+        float least = -kNegInf;
+        for (int i = tid; i < kRoom; i += NT) {
+            const float x = lds.c.v[i];
+            int higher = 0;
+#pragma unroll 8
+            for (int j = 0; j < kRoom; ++j) higher += lds.c.v[j] > x ? 1 : 0;
+            if (higher < n) least = fminf(least, x);
+        }
+        const float of_wave = -lanes::max<64>(-least);
+        if (lanes::lane() == 0) lds.red[tid >> 6] = of_wave;
         __syncthreads();
         last = lds.red[0];
-        for (int i = 1; i < NT / 64; ++i) last = fmaxf(last, lds.red[i]);
-        if (top == last && count > 0) atomicAdd(&lds.n_hot, count);
-        __syncthreads();
-        above = found;
-        found += lds.n_hot;
-        if (last == kNegInf) break;  // fewer than n values
-        __syncthreads();
-    }
-    if (tid == 0) {
-        lds.c.n = 0;
-        lds.n_hot = 0;
-    }
-    __syncthreads();
-    for (int v = part.v0 + tid; v < part.v1; v += NT) {
-        float x[N];
-        Vec<T>::open(load16(base + v * N), x);
-        for (int i = 0; i < N; ++i)
-            if (x[i] > last) lds.c.add(x[i], ps.head + v * N + i);
-    }
-    if (tid < edges) {
-        const float x = Vec<T>::one(z[ps.edge(tid)]);
-        if (x > last) lds.c.add(x, ps.edge(tid));
-    }
-    if (last == kNegInf) {
-        __syncthreads();
-        return;
+        for (int i = 1; i < NT / 64; ++i) last = fminf(last, lds.red[i]);
     }
     // equals in the order of their indexes: the head's edges, pieces, the tail's
     const int need = n - above;
