@@ -337,8 +337,8 @@ struct Segments {
 // among what reaches it: about n to 2 n values, in as many threads' stretches,
 // which the workgroup reads again (from a cache, if the first read went
 // through it).  lds.c.n passes kRoom where that many tie with it or a few
-// stretches hold them; then the rest is not looked at.  Begins behind the barrier that lds.group is written
-// before; ends with one.
+// stretches hold them; then the rest is not looked at.  Begins behind the
+// barrier that lds.group is written before; ends with one.
 // HELD: a part is one take, still in registers.
 template <typename T, int NT, bool HELD>
 __device__ __forceinline__ void gather_best(const T* z, const Pieces<T>& ps, const Part& part, const Segments<NT>& seg,
@@ -502,7 +502,7 @@ enum { TOP_NONE = 0, TOP_LONG = 1, TOP_HELD = 2 };
 // others go on to the next.  256 threads: with 1024 a row's end is too large a
 // share of it.  Four waves a SIMD is what the registers of 32 values and 32 more
 // under way leave without spills (five without alternatives spill: 4096 x 128256
-// bf16 163 us, 200); binary32 with alternatives is held to five (5000 x 9382 46
+// bf16 163 us, 200); binary32 with alternatives is held to five (5000 x 9382 45
 // us, 52 with four).  What the alternatives cost (8 us of 170 with 8) is the
 // row's end: five barriers, and the stretches read again.
 template <typename T, int NT, int MODE>
@@ -606,7 +606,8 @@ __global__ __launch_bounds__(NT, sizeof(T) == 4 && MODE == TOP_LONG ? 5 : 4) voi
         __syncthreads();
         if (TOP) {
             gather_best<T, NT, MODE == TOP_HELD>(z, ps, part, seg, y, one, raw, best, a.top, lds);
-            if (lds.c.n > kRoom) gather_slow<T, NT>(z, ps, part, a.top, lds);
+            // (out of the row's way, or rows without need of it take 2% longer)
+            if (__builtin_expect(lds.c.n > kRoom, 0)) gather_slow<T, NT>(z, ps, part, a.top, lds);
         }
         if (tid >= 64) continue;
         // the waves' sums, a lane each and all of them in every lane
