@@ -11,11 +11,12 @@
 // independent: a quantisation block is a power of two up to the chunk, so its
 // absmax never leaves the workgroup.  Every byte is read once and written
 // once, past the caches; what bounds the step is HBM: 218M bf16 weights with
-// binary32 moments 790 us (22 bytes each, 6.1 TB/s), 51.4M binary32 ones with a
-// bf16 copy 222 us behind the norm (28 bytes, 6.5 TB/s), 19.6M with 8-bit
-// moments 38 us (14 bytes, 7.2 TB/s, some of it cached).  Small tensors are
-// bound by the launch and three loads that wait for each other (chunk, tensor,
-// data): 65 vectors of 2048 4.8 us.
+// binary32 moments 787 us (22 bytes each, 6.1 TB/s), 51.4M binary32 ones with a
+// bf16 copy 220 us behind the norm (28 bytes, 6.5 TB/s), 14.3M with 8-bit
+// moments 36 us (14 bytes, 5.5 TB/s), 51.4M of them 119 us (6.1 TB/s) and with
+// the root of v in their codes 125.  Small tensors are bound by the launch and
+// three loads that wait for each other (chunk, tensor, data): 65 vectors of 2048
+// 4.8 us.
 //
 // Arithmetic: the moments follow the blockwise-int8 step's fixed binary32
 // order with no FMA contraction, and the codes come from correctly rounded

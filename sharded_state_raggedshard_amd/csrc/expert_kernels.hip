@@ -302,8 +302,8 @@ constexpr int kRowThreads = 256;
 // A wave takes a share of a token's row and writes it to its k slots.  Bound by
 // HBM's writes: 16384 x 2880 bf16 to 4 slots 72.5 us (6.5 TB/s), 8192 x 7168 to
 // 8 181 us (5.8 TB/s), and 59 us more for 235 MB of padding rows (segments of
-// 128).  Two pieces a lane: 16384 x 2880 four 76; 2000 x 4096 binary32 to 6
-// 41.5, four 44.
+// 128).  Weights are free (8192 x 7168 182 us with and without).  Two pieces a
+// lane: 16384 x 2880 four 76; 2000 x 4096 binary32 to 6 41.5, four 44.
 constexpr int kDispatchPieces = 2;
 template <typename T, bool WEIGHTED, bool LINES>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(ExpertRows a, const T* x, int64_t ldx, T* y, int64_t ldy,
@@ -355,9 +355,9 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(ExpertRows a, con
 // A wave takes a share of a token's row from its k slots, B of them in flight.
 // Sums are binary32, in the order of the choices.  Bound by HBM's reads: 8192 x
 // 7168 bf16 from 8 slots 178 us, 16384 x 2880 from 4 79 us (5.9 TB/s both; four
-// pieces a lane the same).  bf16 rows of one piece a lane have eight slots in
-// flight (25534 x 264 from 6 30 us, four 36; binary32 has none to gain: 8000 x
-// 250 from 8 19 us, four 15).
+// pieces a lane the same; with rows to add 181 and 84).  bf16 rows of one piece
+// a lane have eight slots in flight (25534 x 264 from 6 30 us, four 36; binary32
+// has none to gain: 8000 x 250 from 8 19 us, four 15).
 constexpr int kCombinePieces = 2;
 template <typename T, int U, bool LINES>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(ExpertRows a, const T* y, int64_t ldy, const T* add,

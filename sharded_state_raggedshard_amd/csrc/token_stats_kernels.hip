@@ -14,10 +14,14 @@
 // of their exponents.
 //
 // Both kernels are bound by HBM where rows are many: 4096 x 128256 bf16 (1.05
-// GB) take 163 us (6.4 TB/s), with 8 alternatives 170 and with 32 194, and
-// their gradient 340 us (6.2 TB/s of 2.1 GB); 6001 x 32003 binary32 119 us and
-// 129 with 8.  Few rows are split over workgroups and joined by a second
-// launch: 16 x 128256 8.9 us, with 20 alternatives 13.4.
+// GB) take 160 us (6.6 TB/s), with 8 alternatives 169 and with 32 182, and
+// their gradient 346 us (6.1 TB/s of 2.1 GB); 6001 x 32003 binary32 116 us and
+// 127 with 8.  Few rows are split over workgroups and joined by a second
+// launch: 16 x 128256 8.1 us, with 20 alternatives 13.2.
+//
+// A row's first loads go out before its token is known, so a row that takes no
+// part still costs them, 16 KB a workgroup: 4096 x 128256 of which half take
+// part 97 us, none 12.5.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
